@@ -66,6 +66,11 @@ enum {
 #define LSA_DEV_TIMEOUT 4       /* a bounded device wait ran out */
 #define LSA_DEV_INDEX 8         /* an index input was out of range and was skipped */
 
+/* Element types, for the entry points that take more than bf16. */
+#define LSA_DTYPE_BF16 0
+#define LSA_DTYPE_F16 1
+#define LSA_DTYPE_F32 2
+
 /* Message of the last error returned on this thread ("" if none). */
 const char *lsa_last_error(void);
 
@@ -84,6 +89,7 @@ const char *lsa_version(void);
  */
 #define LSA_TEST_STALL_ATTENTION 1
 #define LSA_TEST_STALL_INDEXER 2
+#define LSA_TEST_STALL_ATTENTION_Q4 8   /* the latent attention of lsa_sparse_decode_q4 */
 int lsa_test_stall_next_wait(int which);
 
 /*
@@ -427,6 +433,134 @@ int lsa_fetch_chunks(int n_pools, const void *const *host_pools, const size_t *c
  */
 int lsa_advance_window(int32_t *window_start, int32_t *window_len, int B, int by, int new_len,
                        lsa_stream_t stream);
+
+/*
+ * Chunk tables, slot maps and positions from request lengths, on the device (no counterpart
+ * in the paper: the paper's steps start from tables like these).
+ *
+ * Request b has cached_len[b] tokens in the pool and brings new_len[b] more:
+ *   have = ceil(cached / 64), need = ceil((cached + new) / 64)
+ * table_next row b: chunks c < have keep the slot that `table` gives them, chunks
+ * have <= c < need take free slots (slots < n_slots that no kept entry names), in ascending
+ * order of (b, c) and of slot, all other entries become -1.  So a finished request (both
+ * lengths 0) frees its slots.  Several requests may share a chunk that no token is
+ * appended to (a common prefix); a shared chunk that is only partly filled is the caller's to copy.
+ * Token i of request b gets entry new_offset[b] + i of the maps:
+ *   position = cached + i, slot_map = slot * 64 + position % 64 (-1: no slot).
+ * Entries behind the last token are -1 in both, which lsa_qk_norm_rope and lsa_write_q4 skip,
+ * so a batch may be padded to max_new rows.
+ *
+ *   table [B, table_stride] int32 (device); table_next the same shape, another buffer (out)
+ *   cached_len, new_len [B] int32 (device)
+ *   slot_map [max_new] int64, position [max_new] int32 (device, out); new_offset [B + 1] int32 (device, out)
+ *   n_free [1] int32 (device, out): slots still free
+ * dev_status: LSA_DEV_TABLE (a kept chunk has no valid slot; its entry becomes -1),
+ * LSA_DEV_CAPACITY (too few free slots, a request longer than its table row, or more than
+ * max_new new tokens: what does not fit gets -1 or no entry), LSA_DEV_INDEX (a negative
+ * length, taken as 0).  A request is cut to 2^31 - 1 tokens, new_offset to 2^31 - 1.
+ * Supported: 1 <= B <= 65535, table_stride < 2^25, n_slots < 2^31, max_new < 2^30.
+ */
+int lsa_build_tables(const int32_t *table, int table_stride, const int32_t *cached_len, const int32_t *new_len, int B,
+                     int64_t n_slots, int max_new, int32_t *table_next, int64_t *slot_map, int32_t *position,
+                     int32_t *new_offset, int32_t *n_free, int32_t *dev_status, void *ws, size_t ws_bytes,
+                     lsa_stream_t stream);
+size_t lsa_build_tables_workspace_size(int B, int table_stride, int64_t n_slots);
+
+/*
+ * RMS norm of queries and keys for each head, and the position rotation, in one pass.
+ *
+ * For every row x (head_dim values) of q [T, Hq] and k [T, Hk]:
+ *   columns < norm_width:  x / sqrt(mean(x[0 .. norm_width)^2) + eps) * weight   (weight NULL: 1;
+ *     norm_width 0: no norm; other columns as they are)
+ *   columns [rot_offset, rot_offset + rot_dim), after the norm, in pairs (u, v):
+ *     (u, v) <- (u cos a_i - v sin a_i, v cos a_i + u sin a_i),  a_i = position[t] * inv_freq[i]
+ *     i < rot_dim / 2; u and v are columns rot_offset + i and rot_offset + rot_dim / 2 + i, or
+ *     with `interleaved` rot_offset + 2 i and rot_offset + 2 i + 1
+ * Angles are reduced in 64 bits, everything else is fp32, rounded once to the rows' type.
+ * Rows whose position is negative are padding: nothing of them is read into a result and their
+ * output rows stay as they are.  q_out may be q and k_out may be k.
+ *   q, k, q_out, k_out: strides in elements for tokens and heads, columns contiguous; Hq or Hk may be 0
+ *   weights [norm_width] of the rows' type; position [T] int32, inv_freq [rot_dim / 2] fp32 (device)
+ * Supported: bf16, f16, fp32; even head_dim up to 1024; even rot_offset and rot_dim; up to 1024 heads.
+ */
+int lsa_qk_norm_rope(int dtype, int64_t T, int head_dim, const void *q, int64_t q_token_stride, int64_t q_head_stride,
+                     int Hq, const void *q_weight, int q_norm_width, void *q_out, int64_t q_out_token_stride,
+                     int64_t q_out_head_stride, const void *k, int64_t k_token_stride, int64_t k_head_stride, int Hk,
+                     const void *k_weight, int k_norm_width, void *k_out, int64_t k_out_token_stride,
+                     int64_t k_out_head_stride, float eps, const int32_t *position, const float *inv_freq,
+                     int rot_offset, int rot_dim, int interleaved, lsa_stream_t stream);
+
+/*
+ * 4-bit chunk pools.
+ * A row of `width` values (one head of one token) is stored in groups of 16 consecutive
+ * values: e2m1 codes (0, .5, 1, 1.5, 2, 3, 4, 6 and a sign) with one e4m3 scale s a group and one
+ * fp32 scale g for the pool, value = code * s * g.  Rounding, in fp32 and to nearest even:
+ *   s = e4m3(min(amax / (6 g), 448)),  code = e2m1(x / (s g)), saturating; s = 0 stores zeros.
+ * Values beyond 2688 g saturate; a NaN makes its group NaN.
+ * A pool is [n_slots, heads, 36 * width] bytes: per slot and head 64 rows of width / 2 code
+ * bytes (low nibble: even column), then 64 rows of width / 16 scale bytes.  lsa_q4_chunk_bytes is 36 *
+ * width (0 for an unsupported width), so a slot is heads * lsa_q4_chunk_bytes bytes, which is what
+ * lsa_fetch_chunks and lsa_gather_chunks move.
+ * Supported widths: multiples of 16 up to 4096; up to 1024 heads.
+ */
+int64_t lsa_q4_chunk_bytes(int width);
+
+/*
+ * Writes rows into 4-bit pools: row t of k (and of v, if v_pool is given) goes to pool row
+ * slot_map[t] (slot * 64 + row, as lsa_build_tables writes it; -1: skipped; other values outside
+ * the pool are skipped and set LSA_DEV_INDEX).  Entries other than -1 must be distinct: rows that name the same
+ * pool row leave unspecified codes there.
+ *   k [T, heads, k_width], v [T, heads, v_width] bf16, f16 or fp32 (device), strides in
+ *   elements, columns contiguous, rows 16-byte aligned; slot_map [T] int64 (device)
+ */
+int lsa_write_q4(int dtype, int64_t T, int heads, const void *k, int64_t k_token_stride, int64_t k_head_stride,
+                 int k_width, uint8_t *k_pool, float k_scale, const void *v, int64_t v_token_stride,
+                 int64_t v_head_stride, int v_width, uint8_t *v_pool, float v_scale, int64_t n_slots,
+                 const int64_t *slot_map, int32_t *dev_status, lsa_stream_t stream);
+
+/*
+ * lsa_append_token for 4-bit pools: the token at position window_start[b] + window_len[b] of each
+ * sequence is written (new_k [B, heads, k_width], new_v or NULL, contiguous), its indexer key
+ * new_li [B, dl] (or NULL) copied into the bf16 li_pool, and window_len[b] incremented.  A
+ * chunk without a slot sets LSA_DEV_TABLE and leaves that sequence unchanged.
+ */
+int lsa_append_token_q4(int dtype, int heads, const void *new_k, int k_width, uint8_t *k_pool, float k_scale,
+                        const void *new_v, int v_width, uint8_t *v_pool, float v_scale, const lsa_bf16 *new_li,
+                        lsa_bf16 *li_pool, int dl, int64_t n_slots, const int32_t *chunk_table, int table_stride,
+                        const int32_t *window_start, int32_t *window_len, int B, int32_t *dev_status,
+                        lsa_stream_t stream);
+
+/*
+ * Reads rows back: out[t] (heads * width values, bf16, f16 or fp32) = the values of pool row
+ * slot_map[t]; zeros where slot_map[t] is -1 (or outside the pool, which sets LSA_DEV_INDEX).
+ */
+int lsa_read_q4(const uint8_t *pool, int64_t n_slots, int heads, int width, float scale, const int64_t *slot_map,
+                int64_t T, int out_dtype, void *out, int32_t *dev_status, lsa_stream_t stream);
+
+/*
+ * lsa_sparse_decode over 4-bit pools, with grouped heads.
+ * The row set, the softmax and the lse are those of lsa_sparse_decode: the top-k rows of sequence b, then the
+ * positions window_start[b] .. + window_len[b] - 1 (any start; a whole context is the window from
+ * position 0 with k = 0).  Query head h reads K/V head h / (Hq / heads).  Latent layout
+ * (v_pool == NULL): V is the first dv columns of the k_pool row, and v_scale is not used.
+ * Pool rows outside the row set are never read into a result, whatever they hold.  A
+ * sequence without rows gives out = 0, lse = -inf.
+ *   q [B, Hq, dqk] bf16 or f16; out [B, Hq, dv] bf16, f16 or fp32; lse [B, Hq] fp32 (optional)
+ *   max_window_len: host upper bound of window_len[b]; it sizes the split-K grid only
+ * Softmax weights enter the value product as f16 (11 significant bits); scores, sums and
+ * outputs accumulate in fp32.
+ * dev_status: LSA_DEV_TABLE (a needed chunk has no valid slot: its rows are skipped),
+ * LSA_DEV_INDEX (a negative position: skipped; a negative window_start: no window), LSA_DEV_TIMEOUT.
+ * Supported: (dqk, dv) = (64, 64) or (128, 128) with separate pools and any Hq up to 1024 that is a
+ * multiple of heads; (576, 512) latent with heads = 1 and 1 <= Hq <= 128.
+ */
+int lsa_sparse_decode_q4(int q_dtype, const void *q, const uint8_t *k_pool, float k_scale, const uint8_t *v_pool,
+                         float v_scale, int64_t n_slots, int heads, const int32_t *chunk_table, int table_stride,
+                         const int32_t *topk_idx, const int32_t *topk_count, int k, const int32_t *window_start,
+                         const int32_t *window_len, int max_window_len, int B, int Hq, int dqk, int dv, float scale,
+                         int out_dtype, void *out, float *lse, int32_t *dev_status, void *ws, size_t ws_bytes,
+                         lsa_stream_t stream);
+size_t lsa_sparse_decode_q4_workspace_size(int B, int Hq, int heads, int dqk, int dv, int k, int max_window_len);
 
 /*
  * a7 (offline) -- cross-layer majority-vote labels for one decode window.

@@ -44,6 +44,9 @@ int take_test_stall(int which);
             return ::lsa::fail(LSA_ERR_CUDA, "%s: %s", #call, cudaGetErrorString(e_)); \
     } while (0)
 
+__host__ __device__ inline int64_t lsa_min64(int64_t a, int64_t b) { return a < b ? a : b; }
+__host__ __device__ inline int64_t lsa_max64(int64_t a, int64_t b) { return a > b ? a : b; }
+
 inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
 // Carves consecutive 256-byte aligned regions out of a caller workspace.

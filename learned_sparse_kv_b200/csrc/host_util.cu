@@ -64,7 +64,7 @@ bool take_copy_failure() {
 extern "C" const char *lsa_last_error(void) { return lsa::g_last_error; }
 
 extern "C" int lsa_test_stall_next_wait(int which) {
-    if (which != LSA_TEST_STALL_ATTENTION && which != LSA_TEST_STALL_INDEXER)
+    if (which != LSA_TEST_STALL_ATTENTION && which != LSA_TEST_STALL_INDEXER && which != LSA_TEST_STALL_ATTENTION_Q4)
         return lsa::fail(LSA_ERR_INVALID_ARG, "lsa_test_stall_next_wait: unknown kernel %d", which);
     lsa::g_test_stall.fetch_or(which);
     return LSA_OK;

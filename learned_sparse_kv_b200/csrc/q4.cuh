@@ -1,0 +1,126 @@
+// q4.cuh -- the 4-bit chunk pools: layout and conversions.
+//
+// A row of W values (one head of one token) is W / 16 groups of 16 consecutive values.  A
+// value is an e2m1 code (0, .5, 1, 1.5, 2, 3, 4, 6 with a sign), a group has one e4m3 scale s,
+// the pool one fp32 scale g:  value = e2m1 * s * g.  9 bits for two values: 0.5625 byte each.
+// A chunk of one head is 36 W contiguous bytes: 64 code rows of W / 2 bytes (low nibble: even
+// column), then 64 scale rows of W / 16 bytes, so that a window chunk is one contiguous block
+// and a single row two pieces.  A pool is [n_slots, heads, 36 W].
+//
+// e2m1 * e4m3 has at most 6 significant bits and lies between 2^-10 and 2688, so every value
+// (before g) is exact in f16 and in bf16: dequantising rounds nothing.
+#pragma once
+#include <cuda_fp16.h>
+
+#include "common.cuh"
+
+namespace lsa {
+namespace q4 {
+
+constexpr int GROUP = 16;
+constexpr float E2M1_MAX = 6.f, E4M3_MAX = 448.f;
+
+__host__ __device__ constexpr int64_t chunk_bytes(int W) { return 36 * (int64_t)W; }
+__host__ __device__ constexpr int code_row(int W) { return W / 2; }
+__host__ __device__ constexpr int scale_row(int W) { return W / GROUP; }
+__host__ __device__ constexpr int scale_base(int W) { return LSA_CHUNK * (W / 2); }
+
+// Eight e2m1 codes (nibble 2i and 2i + 1 in byte i) -> four f16 pairs.
+__device__ __forceinline__ void e2m1x8_to_f16(uint32_t w, uint32_t (&h)[4]) {
+    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+        "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
+        : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+        : "r"(w));
+}
+
+// Two e4m3 bytes -> an f16 pair (low byte in the low half).
+__device__ __forceinline__ uint32_t e4m3x2_to_f16(uint32_t two) {
+    uint32_t h;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)two));
+    return h;
+}
+
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+
+// The low / high half of an f16 pair in both halves.
+__device__ __forceinline__ uint32_t dup_lo(uint32_t h) { return __byte_perm(h, h, 0x1010); }
+__device__ __forceinline__ uint32_t dup_hi(uint32_t h) { return __byte_perm(h, h, 0x3232); }
+
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+    uint32_t d;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+    return d;
+}
+
+// The 16 values of one group as 8 code bytes and the e4m3 scale byte.
+//   s = e4m3(min(amax / (6 g), 448)),  code = e2m1(x / (s g)), both to nearest even and
+//   saturating; s = 0 stores zeros.  amax / 6 and x / s often lie exactly halfway between two
+//   codes, so both quotients are true (correctly rounded) divisions, never products with a
+//   rounded reciprocal.  A NaN in the group gives a NaN scale: the whole group reads as NaN.
+//   An infinity saturates the scale; the finite values of its group then read as they round.
+__device__ __forceinline__ uint2 quantise_group(const float (&x)[16], float g, float g6, uint32_t &scale_byte) {
+    float amax = 0.f;
+    bool nan = false;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        amax = fmaxf(amax, fabsf(x[i]));
+        nan |= x[i] != x[i];
+    }
+    const float t = fminf(__fdiv_rn(amax, g6), E4M3_MAX);
+    uint16_t e;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(e) : "f"(0.f), "f"(t));
+    const uint32_t sh = e4m3x2_to_f16(e);
+    const float sg = __half2float(__ushort_as_half((uint16_t)sh)) * g;
+    scale_byte = nan ? 0x7fu : (e & 0xffu);
+    uint2 codes = make_uint2(0u, 0u);
+    if (sg > 0.f) {
+        uint32_t w[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            float y[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) y[i] = __fdiv_rn(x[8 * j + i], sg);
+            asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+                "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\t"
+                "cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n\t"
+                "cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n\t"
+                "cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n\t"
+                "mov.b32 %0, {b0, b1, b2, b3};\n\t}"
+                : "=r"(w[j])
+                : "f"(y[0]), "f"(y[1]), "f"(y[2]), "f"(y[3]), "f"(y[4]), "f"(y[5]), "f"(y[6]), "f"(y[7]));
+        }
+        codes = make_uint2(w[0], w[1]);
+    }
+    return codes;
+}
+
+}  // namespace q4
+
+// Element types of the entry points that take more than bf16 (LSA_DTYPE_*).
+template <class T> __device__ __forceinline__ float to_f32(T v);
+template <> __device__ __forceinline__ float to_f32<float>(float v) { return v; }
+template <> __device__ __forceinline__ float to_f32<__half>(__half v) { return __half2float(v); }
+template <> __device__ __forceinline__ float to_f32<__nv_bfloat16>(__nv_bfloat16 v) { return __bfloat162float(v); }
+template <class T> __device__ __forceinline__ T from_f32(float v);
+template <> __device__ __forceinline__ float from_f32<float>(float v) { return v; }
+template <> __device__ __forceinline__ __half from_f32<__half>(float v) { return __float2half_rn(v); }
+template <> __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+
+// N consecutive elements as one or more aligned vector accesses of up to 16 bytes.
+template <class T, int N>
+struct alignas(sizeof(T) * N < 16 ? sizeof(T) * N : 16) Vec {
+    T v[N];
+};
+
+inline int dtype_size(int dtype) { return dtype == LSA_DTYPE_F32 ? 4 : 2; }
+inline bool dtype_known(int dtype) { return dtype >= LSA_DTYPE_BF16 && dtype <= LSA_DTYPE_F32; }
+
+}  // namespace lsa

@@ -1,0 +1,92 @@
+// q4_rows.cuh -- the row set of one sequence of the 4-bit attention, in units of 64 rows, and
+// the parameters shared by its kernels.
+#pragma once
+#include "q4.cuh"
+
+namespace lsa {
+namespace q4 {
+
+struct DecodeParams {
+    const void *q;                  // [B, Hq, dqk] bf16 or f16
+    const uint8_t *k_pool, *v_pool; // v_pool null: latent rows
+    const int32_t *table, *topk_idx, *topk_count, *window_start, *window_len;
+    float *o_part, *m_part, *l_part;   // [B, splits, Hq, dv], [B, splits, Hq]
+    int32_t *status;
+    int64_t n_slots;
+    int table_stride, k, Hq, heads, n_splits;
+    float scale_log2, v_scale;      // scale_log2: scale * k_scale * log2(e)
+    int q_f16;
+};
+
+// Units of one sequence: ceil(tk / 64) units of 64 top-k rows, then the window chunk by chunk
+// (its first and last chunk may be partly outside the window).
+struct Units {
+    int tk, wstart, wlen, t_topk, first_chunk, total;
+    __device__ Units(const DecodeParams &p, int b) {
+        tk = p.k > 0 ? min(max(p.topk_count[b], 0), p.k) : 0;
+        wstart = p.window_start[b];
+        wlen = max(p.window_len[b], 0);
+        if (wstart < 0) {            // a window before position 0 does not exist
+            if (wlen > 0 && threadIdx.x == 0) flag(p.status, LSA_DEV_INDEX);
+            wstart = wlen = 0;
+        }
+        wlen = min(wlen, INT32_MAX - 63 - wstart);
+        t_topk = (tk + LSA_CHUNK - 1) / LSA_CHUNK;
+        first_chunk = wstart / LSA_CHUNK;
+        total = t_topk + (wlen > 0 ? (wstart + wlen - 1) / LSA_CHUNK - first_chunk + 1 : 0);
+    }
+    // Pool slot of window unit u, or -1.
+    __device__ int window_slot(const DecodeParams &p, int b, int u) const {
+        const int chunk = first_chunk + (u - t_topk);
+        const int slot = chunk < p.table_stride ? __ldg(p.table + (size_t)b * p.table_stride + chunk) : -1;
+        if (slot >= 0 && slot < p.n_slots) return slot;
+        flag(p.status, LSA_DEV_TABLE);
+        return -1;
+    }
+    // Is row i of window unit u inside the window?
+    __device__ bool in_window(int u, int i) const {
+        const int pos = (first_chunk + (u - t_topk)) * LSA_CHUNK + i;
+        return pos >= wstart && pos - wstart < wlen;
+    }
+    // Pool row (slot * 64 + row) of row i of top-k unit u, or -1.
+    __device__ int64_t topk_row(const DecodeParams &p, int b, int u, int i) const {
+        const int r = u * LSA_CHUNK + i;
+        if (r >= tk) return -1;
+        const int pos = __ldg(p.topk_idx + (size_t)b * p.k + r);
+        if (pos < 0) { flag(p.status, LSA_DEV_INDEX); return -1; }
+        const int chunk = pos / LSA_CHUNK;
+        const int slot = chunk < p.table_stride ? __ldg(p.table + (size_t)b * p.table_stride + chunk) : -1;
+        if (slot >= 0 && slot < p.n_slots) return (int64_t)slot * LSA_CHUNK + (pos % LSA_CHUNK);
+        flag(p.status, LSA_DEV_TABLE);
+        return -1;
+    }
+};
+
+// Softmax weights enter P V as f16: exp2(s - m_ref + P_SHIFT), where the reference m_ref follows
+// the row maximum only when that has grown by more than 2^RESCALE (so O is rarely rescaled).
+// The largest weight is 2^(P_SHIFT + RESCALE) = 2^14 < 65504; a weight stays a normal f16
+// number, 11 significant bits, down to 2^-20 of the largest.  Rounding it so leaves a relative
+// error of 2^-12 on each weight, an eighth of what rounding a bf16 result leaves.
+constexpr float RESCALE = 8.f, P_SHIFT = 6.f;
+
+// Queries enter Q K^T as f16 after a division by a power of two that brings the largest entry
+// of the row into [1, 2): bf16 has fewer significant bits than f16, so entries down to 2^-16 of the
+// largest are exact and the rest are off by at most 2^-25 of it.
+__device__ __forceinline__ float row_exponent(float amax, float &inv) {
+    const uint32_t e = (__float_as_uint(amax) >> 23) & 255u;
+    if (e == 0u || e >= 254u) { inv = 1.f; return 1.f; }   // zero, subnormal, infinite or NaN
+    inv = __uint_as_float((254u - e) << 23);
+    return __uint_as_float(e << 23);
+}
+
+// Writes out = sum_r 2^(m_r - M) O_r / sum and the natural-log LSE from the splits' partials.
+int launch_merge(const DecodeParams &p, int B, int dv, int out_dtype, void *out, float *lse, cudaStream_t stream);
+
+}  // namespace q4
+
+namespace q4mla {
+int launch(const q4::DecodeParams &p, int B, cudaStream_t stream);
+int splits(int B, int max_units);
+}  // namespace q4mla
+
+}  // namespace lsa

@@ -56,6 +56,16 @@ def _load():
         "lsa_advance_window": ([P, P, I, I, I, P], I),
         "lsa_label_vote": ([P, I, I, I, F, I, I, P, P, P, SZ, P], I),
         "lsa_label_vote_workspace_size": ([I, I, I], SZ),
+        "lsa_build_tables": ([P, I, P, P, I, I64, I, P, P, P, P, P, P, P, SZ, P], I),
+        "lsa_build_tables_workspace_size": ([I, I, I64], SZ),
+        "lsa_qk_norm_rope": ([I, I64, I, P, I64, I64, I, P, I, P, I64, I64, P, I64, I64, I, P, I, P, I64, I64, F, P, P, I,
+                              I, I, P], I),
+        "lsa_q4_chunk_bytes": ([I], I64),
+        "lsa_write_q4": ([I, I64, I, P, I64, I64, I, P, F, P, I64, I64, I, P, F, I64, P, P, P], I),
+        "lsa_append_token_q4": ([I, I, P, I, P, F, P, I, P, F, P, P, I, I64, P, I, P, P, I, P, P], I),
+        "lsa_read_q4": ([P, I64, I, I, F, P, I64, I, P, P, P], I),
+        "lsa_sparse_decode_q4": ([I, P, P, F, P, F, I64, I, P, I, P, P, I, P, P, I, I, I, I, I, F, I, P, P, P, P, SZ, P], I),
+        "lsa_sparse_decode_q4_workspace_size": ([I, I, I, I, I, I, I], SZ),
         "lsa_last_error": ([], ctypes.c_char_p),
         "lsa_version": ([], ctypes.c_char_p),
         "lsa_test_stall_next_wait": ([I], I),
@@ -75,7 +85,7 @@ def version() -> str:
     return _lib.lsa_version().decode()
 
 
-TEST_STALL_ATTENTION, TEST_STALL_INDEXER = 1, 2
+TEST_STALL_ATTENTION, TEST_STALL_INDEXER, TEST_STALL_ATTENTION_Q4 = 1, 2, 8
 
 
 def test_stall_next_wait(which):
@@ -422,6 +432,297 @@ def advance_window(window_start, window_len, by, new_len, *, stream=None):
     _dev(window_start, torch.int32, "window_start"); _dev(window_len, torch.int32, "window_len")
     _check(_lib.lsa_advance_window(_ptr(window_start), _ptr(window_len), window_start.numel(), by, new_len,
                                    _stream(stream)))
+
+
+# ------------------------------------------- tables, norm + rotation ----
+
+DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+
+
+def _dtype(dt, name):
+    if dt not in DTYPES:
+        raise LSAError(1, f"{name} must be bfloat16, float16 or float32, got {dt}")
+    return DTYPES[dt]
+
+
+def _shape(t, shape, name):
+    if tuple(t.shape) != tuple(shape):
+        raise LSAError(1, f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _same_device(dev, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.device != dev:
+            raise LSAError(1, f"{name} must be on {dev}, like the first argument")
+
+
+def _launch(dev, stream):
+    """The stream handle for a launch on `dev`, whatever the current device is."""
+    return _stream(stream if stream is not None else torch.cuda.current_stream(dev))
+
+
+def _side(stream, dev, *fresh):
+    """Tensors made here on the current stream stay reserved until the work on `stream` is done."""
+    if stream is not None and stream != torch.cuda.current_stream(dev):
+        for t in fresh:
+            t.record_stream(stream)
+
+
+def build_tables_workspace_size(B, table_stride, n_slots):
+    return _lib.lsa_build_tables_workspace_size(B, table_stride, n_slots)
+
+
+def build_tables(table, cached_len, new_len, n_slots, max_new, *, table_next=None, slot_map=None, position=None,
+                 new_offset=None, n_free=None, status=None, ws=None, stream=None):
+    """Chunk table, slot map and positions of requests with cached_len[b] tokens in the pool and new_len[b] more.
+
+    table [B, stride] int32 (-1: none), cached_len, new_len [B] int32.  Returns (table_next [B, stride] int32,
+    slot_map [max_new] int64, position [max_new] int32, new_offset [B + 1] int32, n_free [1] int32); map entries behind
+    the last new token are -1.
+    """
+    _dev(table, torch.int32, "table"); _dev(cached_len, torch.int32, "cached_len"); _dev(new_len, torch.int32, "new_len")
+    B, stride = table.shape
+    _shape(cached_len, (B,), "cached_len"); _shape(new_len, (B,), "new_len")
+    dev = table.device
+    i32 = dict(dtype=torch.int32, device=dev)
+    with torch.cuda.device(dev):
+        table_next = torch.empty(B, stride, **i32) if table_next is None else _dev(table_next, torch.int32, "table_next")
+        slot_map = torch.empty(max_new, dtype=torch.int64, device=dev) if slot_map is None else \
+            _dev(slot_map, torch.int64, "slot_map")
+        position = torch.empty(max_new, **i32) if position is None else _dev(position, torch.int32, "position")
+        new_offset = torch.empty(B + 1, **i32) if new_offset is None else _dev(new_offset, torch.int32, "new_offset")
+        n_free = torch.empty(1, **i32) if n_free is None else _dev(n_free, torch.int32, "n_free")
+        _shape(table_next, (B, stride), "table_next"); _shape(slot_map, (max_new,), "slot_map")
+        _shape(position, (max_new,), "position"); _shape(new_offset, (B + 1,), "new_offset"); _shape(n_free, (1,), "n_free")
+        _same_device(dev, cached_len=cached_len, new_len=new_len, table_next=table_next, slot_map=slot_map,
+                     position=position, new_offset=new_offset, n_free=n_free, status=status, ws=ws)
+        ws = _ws(build_tables_workspace_size(B, stride, n_slots), dev, ws)
+        _check(_lib.lsa_build_tables(_ptr(table), stride, _ptr(cached_len), _ptr(new_len), B, n_slots, max_new,
+                                     _ptr(table_next), _ptr(slot_map), _ptr(position), _ptr(new_offset), _ptr(n_free),
+                                     _ptr(status), _ptr(ws), ws.numel(), _launch(dev, stream)))
+        _side(stream, dev, ws, table_next, slot_map, position, new_offset, n_free)
+    return table_next, slot_map, position, new_offset, n_free
+
+
+def _rows(t, name, dtype, T, D, heads=None):
+    """Checks [T, heads, D] rows with contiguous columns; returns (token stride, head stride)."""
+    if not (isinstance(t, torch.Tensor) and t.is_cuda):
+        raise LSAError(1, f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise LSAError(1, f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() != 3 or t.shape[0] != T or t.shape[2] != D or (heads is not None and t.shape[1] != heads):
+        raise LSAError(1, f"{name} must be [{T}, {'heads' if heads is None else heads}, {D}], got {tuple(t.shape)}")
+    if t.numel() and t.stride(2) != 1:
+        raise LSAError(1, f"{name} must have contiguous columns")
+    # the stride of a dimension of one row is never used; torch may report anything for it
+    return t.stride(0) if T > 1 else 0, t.stride(1) if t.shape[1] > 1 else 0
+
+
+def qk_norm_rope(q, k, position, inv_freq, *, q_weight=None, k_weight=None, q_norm_width=None, k_norm_width=None,
+                 eps=1e-6, rot_offset=0, interleaved=False, q_out=None, k_out=None, stream=None):
+    """RMS norm of q and k for each head and position rotation, in one pass.
+
+    q [T, Hq, D], k [T, Hk, D] (bf16, f16 or fp32, columns contiguous; k may be None), position [T] int32 (negative:
+    padding, the output row stays as it is), inv_freq [rot_dim / 2] fp32.  The norm covers the first q_norm_width /
+    k_norm_width columns (default: the weight's length, or none without a weight); the rotation covers columns
+    [rot_offset, rot_offset + rot_dim).  Returns (q_out, k_out); outputs may be the inputs.
+    """
+    if not (isinstance(q, torch.Tensor) and q.is_cuda and q.dim() == 3):
+        raise LSAError(1, "q must be a CUDA tensor [T, heads, D]")
+    T, Hq, D = q.shape
+    dt, dev = q.dtype, q.device
+    code = _dtype(dt, "q")
+    _dev(position, torch.int32, "position"); _dev(inv_freq, torch.float32, "inv_freq")
+    _shape(position, (T,), "position")
+    if inv_freq.dim() != 1:
+        raise LSAError(1, "inv_freq must have one dimension")
+    widths = []
+    for name, w, n in (("q_weight", q_weight, q_norm_width), ("k_weight", k_weight, k_norm_width)):
+        if w is not None:
+            _dev(w, dt, name)
+        n = (0 if w is None else w.numel()) if n is None else int(n)
+        if w is not None and n > 0:
+            _shape(w, (n,), name)
+        widths.append(n)
+    with torch.cuda.device(dev):
+        q_out = torch.empty_like(q, memory_format=torch.contiguous_format) if q_out is None else q_out
+        if k is not None and k_out is None:
+            k_out = torch.empty_like(k, memory_format=torch.contiguous_format)
+        qs, qo = _rows(q, "q", dt, T, D), _rows(q_out, "q_out", dt, T, D, Hq)
+        ks, ko, Hk = (0, 0), (0, 0), 0
+        if k is not None:
+            ks = _rows(k, "k", dt, T, D)
+            Hk = k.shape[1]
+            ko = _rows(k_out, "k_out", dt, T, D, Hk)
+        _same_device(dev, k=k, position=position, inv_freq=inv_freq, q_weight=q_weight, k_weight=k_weight, q_out=q_out,
+                     k_out=k_out)
+        _check(_lib.lsa_qk_norm_rope(code, T, D, _ptr(q), *qs, Hq, _ptr(q_weight), widths[0], _ptr(q_out), *qo, _ptr(k),
+                                     *ks, Hk, _ptr(k_weight), widths[1], _ptr(k_out), *ko, float(eps), _ptr(position),
+                                     _ptr(inv_freq), int(rot_offset), 2 * inv_freq.numel(), int(bool(interleaved)),
+                                     _launch(dev, stream)))
+        _side(stream, dev, q_out, *([] if k_out is None else [k_out]))
+    return q_out, k_out
+
+
+# ------------------------------------------------------- 4-bit pools ----
+
+def q4_chunk_bytes(width):
+    """Bytes of one chunk (64 rows) of one head in a 4-bit pool."""
+    n = _lib.lsa_q4_chunk_bytes(int(width))
+    if n == 0:
+        raise LSAError(2, f"unsupported 4-bit row width {width} (a multiple of 16 up to 4096)")
+    return n
+
+
+def q4_pool(n_slots, heads, width, device="cuda"):
+    """A zeroed 4-bit pool of n_slots chunks: [n_slots, heads, 36 * width] uint8."""
+    return torch.zeros(n_slots, heads, q4_chunk_bytes(width), dtype=torch.uint8, device=device)
+
+
+def _pool(t, name, heads=None, width=None, n_slots=None):
+    _dev(t, torch.uint8, name)
+    if t.dim() != 3 or t.shape[2] % 576 or t.shape[2] == 0:
+        raise LSAError(1, f"{name} must be a 4-bit pool [n_slots, heads, 36 * width], got {tuple(t.shape)}")
+    for what, n, dim in (("slots", n_slots, 0), ("heads", heads, 1)):
+        if n is not None and t.shape[dim] != n:
+            raise LSAError(1, f"{name} must have {n} {what}, got {t.shape[dim]}")
+    if width is not None and t.shape[2] != 36 * width:
+        raise LSAError(1, f"{name} must hold rows of {width} values, got {t.shape[2] // 36}")
+    return t
+
+
+def _q4_rows(x, name):
+    """[T, width] rows are one head."""
+    if not (isinstance(x, torch.Tensor) and x.is_cuda and x.dim() in (2, 3)):
+        raise LSAError(1, f"{name} must be a CUDA tensor [T, heads, width] or [T, width]")
+    return x.unsqueeze(1) if x.dim() == 2 else x
+
+
+def write_q4(k, k_pool, slot_map, *, v=None, v_pool=None, k_scale=1.0, v_scale=1.0, status=None, stream=None):
+    """Quantises rows k [T, heads, width] (and v) into 4-bit pools at slot_map [T] int64 (slot * 64 + row, -1: skip)."""
+    k = _q4_rows(k, "k")
+    T, heads, kw = k.shape
+    dt, dev = k.dtype, k.device
+    code = _dtype(dt, "k")
+    _dev(slot_map, torch.int64, "slot_map"); _shape(slot_map, (T,), "slot_map")
+    _pool(k_pool, "k_pool", heads, kw)
+    ks, vs, vw = _rows(k, "k", dt, T, kw), (0, 0), 0
+    if (v is None) != (v_pool is None):
+        raise LSAError(1, "v and v_pool come together")
+    if v is not None:
+        v = _q4_rows(v, "v")
+        vw = v.shape[2]
+        vs = _rows(v, "v", dt, T, vw, heads)
+        _pool(v_pool, "v_pool", heads, vw, k_pool.shape[0])
+    _same_device(dev, k_pool=k_pool, slot_map=slot_map, v=v, v_pool=v_pool, status=status)
+    with torch.cuda.device(dev):
+        _check(_lib.lsa_write_q4(code, T, heads, _ptr(k), *ks, kw, _ptr(k_pool), float(k_scale), _ptr(v), *vs, vw,
+                                 _ptr(v_pool), float(v_scale), k_pool.shape[0], _ptr(slot_map), _ptr(status),
+                                 _launch(dev, stream)))
+
+
+def append_token_q4(new_k, new_v, new_li, k_pool, v_pool, li_pool, chunk_table, window_start, window_len, *,
+                    k_scale=1.0, v_scale=1.0, status=None, stream=None):
+    """append_token for 4-bit pools: new_k [B, heads, width] (or [B, width]), new_v likewise or None (latent)."""
+    new_k = _q4_rows(new_k, "new_k")
+    B, heads, kw = new_k.shape
+    dt, dev = new_k.dtype, new_k.device
+    code = _dtype(dt, "new_k")
+    _dev(new_k, dt, "new_k"); _pool(k_pool, "k_pool", heads, kw)
+    vw, dl = 0, 0
+    if (new_v is None) != (v_pool is None):
+        raise LSAError(1, "new_v and v_pool come together")
+    if new_v is not None:
+        new_v = _dev(_q4_rows(new_v, "new_v"), dt, "new_v")
+        vw = new_v.shape[2]
+        _shape(new_v, (B, heads, vw), "new_v"); _pool(v_pool, "v_pool", heads, vw, k_pool.shape[0])
+    if new_li is not None or li_pool is not None:
+        _dev(new_li, torch.bfloat16, "new_li"); _dev(li_pool, torch.bfloat16, "li_pool")
+        dl = li_pool.shape[-1]
+        _shape(new_li, (B, dl), "new_li"); _shape(li_pool, (k_pool.shape[0], CHUNK, dl), "li_pool")
+    for name, t in (("chunk_table", chunk_table), ("window_start", window_start), ("window_len", window_len)):
+        _dev(t, torch.int32, name)
+    stride = chunk_table.shape[-1]
+    _shape(chunk_table, (B, stride), "chunk_table"); _shape(window_start, (B,), "window_start")
+    _shape(window_len, (B,), "window_len")
+    _same_device(dev, new_v=new_v, new_li=new_li, k_pool=k_pool, v_pool=v_pool, li_pool=li_pool,
+                 chunk_table=chunk_table, window_start=window_start, window_len=window_len, status=status)
+    with torch.cuda.device(dev):
+        _check(_lib.lsa_append_token_q4(code, heads, _ptr(new_k), kw, _ptr(k_pool), float(k_scale), _ptr(new_v), vw,
+                                        _ptr(v_pool), float(v_scale), _ptr(new_li), _ptr(li_pool), dl, k_pool.shape[0],
+                                        _ptr(chunk_table), stride, _ptr(window_start), _ptr(window_len), B,
+                                        _ptr(status), _launch(dev, stream)))
+
+
+def read_q4(pool, slot_map, *, scale=1.0, out=None, out_dtype=torch.bfloat16, status=None, stream=None):
+    """Rows slot_map [T] of a 4-bit pool as values [T, heads, width] (zeros where slot_map is -1)."""
+    _pool(pool, "pool"); _dev(slot_map, torch.int64, "slot_map")
+    n_slots, heads, nb = pool.shape
+    dev, T = pool.device, slot_map.numel()
+    _shape(slot_map, (T,), "slot_map")
+    with torch.cuda.device(dev):
+        if out is None:
+            out = torch.empty(T, heads, nb // 36, dtype=out_dtype, device=dev)
+        code = _dtype(out.dtype, "out")
+        _dev(out, out.dtype, "out"); _shape(out, (T, heads, nb // 36), "out")
+        _same_device(dev, slot_map=slot_map, out=out, status=status)
+        _check(_lib.lsa_read_q4(_ptr(pool), n_slots, heads, nb // 36, float(scale), _ptr(slot_map), T, code, _ptr(out),
+                                _ptr(status), _launch(dev, stream)))
+        _side(stream, dev, out)
+    return out
+
+
+def sparse_decode_q4_workspace_size(B, Hq, heads, dqk, dv, k, max_window_len):
+    return _lib.lsa_sparse_decode_q4_workspace_size(B, Hq, heads, dqk, dv, k, max_window_len)
+
+
+def sparse_decode_q4(q, k_pool, v_pool, chunk_table, topk_idx, topk_count, window_start, window_len, max_window_len,
+                     dv, scale, *, k_scale=1.0, v_scale=1.0, out=None, out_dtype=torch.bfloat16, lse=None,
+                     want_lse=True, status=None, ws=None, stream=None):
+    """sparse_decode over 4-bit pools.  q [B, Hq, dqk] bf16 or f16; k_pool [slots, heads, 36 * dqk]; v_pool None (latent)
+    or [slots, heads, 36 * dv].  topk_idx may be None (the window only; from position 0 it is the whole context).
+
+    Returns (out [B, Hq, dv] of out_dtype, lse [B, Hq] fp32 or None).
+    """
+    if not (isinstance(q, torch.Tensor) and q.is_cuda and q.dim() == 3):
+        raise LSAError(1, "q must be a CUDA tensor [B, Hq, dqk]")
+    B, Hq, dqk = q.shape
+    dev = q.device
+    q_code = _dtype(q.dtype, "q")
+    _dev(q, q.dtype, "q"); _pool(k_pool, "k_pool", width=dqk)
+    n_slots, heads, _ = k_pool.shape
+    if v_pool is not None:
+        _pool(v_pool, "v_pool", heads, dv, n_slots)
+    k = 0
+    if topk_idx is not None:
+        _dev(topk_idx, torch.int32, "topk_idx"); _dev(topk_count, torch.int32, "topk_count")
+        k = topk_idx.shape[-1]
+        _shape(topk_idx, (B, k), "topk_idx"); _shape(topk_count, (B,), "topk_count")
+    for name, t in (("chunk_table", chunk_table), ("window_start", window_start), ("window_len", window_len)):
+        _dev(t, torch.int32, name)
+    stride = chunk_table.shape[-1]
+    _shape(chunk_table, (B, stride), "chunk_table"); _shape(window_start, (B,), "window_start")
+    _shape(window_len, (B,), "window_len")
+    with torch.cuda.device(dev):
+        if out is None:
+            out = torch.empty(B, Hq, dv, dtype=out_dtype, device=dev)
+        o_code = _dtype(out.dtype, "out")
+        _dev(out, out.dtype, "out"); _shape(out, (B, Hq, dv), "out")
+        if lse is None and want_lse:
+            lse = torch.empty(B, Hq, dtype=torch.float32, device=dev)
+        if lse is not None:
+            _dev(lse, torch.float32, "lse"); _shape(lse, (B, Hq), "lse")
+        _same_device(dev, k_pool=k_pool, v_pool=v_pool, chunk_table=chunk_table, topk_idx=topk_idx,
+                     topk_count=topk_count, window_start=window_start, window_len=window_len, out=out, lse=lse,
+                     status=status, ws=ws)
+        ws = _ws(sparse_decode_q4_workspace_size(B, Hq, heads, dqk, dv, k, max_window_len), dev, ws)
+        _check(_lib.lsa_sparse_decode_q4(q_code, _ptr(q), _ptr(k_pool), float(k_scale), _ptr(v_pool), float(v_scale),
+                                         n_slots, heads, _ptr(chunk_table), stride, _ptr(topk_idx if k else None),
+                                         _ptr(topk_count if k else None), k, _ptr(window_start), _ptr(window_len),
+                                         max_window_len, B, Hq, dqk, dv, float(scale), o_code, _ptr(out), _ptr(lse),
+                                         _ptr(status), _ptr(ws), ws.numel(), _launch(dev, stream)))
+        _side(stream, dev, ws, out, *([] if lse is None else [lse]))
+    return out, lse
 
 
 # ------------------------------------------------------------------- a7 ----
