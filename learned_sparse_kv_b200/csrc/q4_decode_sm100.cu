@@ -13,15 +13,17 @@
 //   O += P V    N = 256 value columns: CTA r dequantises all 128 rows of its value columns
 //               128r..128r+127 and 256+128r.. (64 KB)
 // N = 128 because a pair MMA costs the same 45 cycles at N = 64 and at N = 128.  With Q (72 KB) and P
-// (16 KB) that is all of shared memory, so K and V have one stage each: K of the next tile is
-// written while P V runs, V of the next one while Q K^T runs.  The codes of the next tile
-// are already in registers by then, and the slots of the one after are being looked up.
+// (16 KB) that is all of shared memory, so K and V have one stage each, handed over in parts: K
+// in three groups of 192 columns, V and P unit by unit.  A part of the next tile is written
+// as soon as the MMAs that read it are done, while the MMAs of the other parts run.  The
+// codes of the next tile are in registers by then, the slots of the one after are being loaded.
 // TMEM per CTA: two S buffers of 64 columns and O = 64 heads x 512 values in 256 columns.
 // Warp roles:
-//   0      S = Q K^T issuer (even CTA)     1   O += P V issuer (even CTA)
-//   2      TMEM allocator
+//   0      MMA issuer (even CTA)            2   TMEM allocator
 //   4..7   softmax, O rescale, epilogue (one thread per TMEM lane: head x unit of the tile)
-//   8..11  dequantise K                    12..15  dequantise V, row masks
+//   8..15  dequantise K                    16..23  dequantise V, row masks
+// (Eight warps each: with four the conversion, a chain of dependent instructions, took 3000
+// cycles a tile and paced the pipeline while the issue slots were 25 % used.)
 // Every mbarrier wait is bounded: on timeout the kernel sets LSA_DEV_TIMEOUT and the abort flag of
 // both CTAs, the other waits return, the MMAs issued so far complete, and the pair exits.  No
 // copy is asynchronous (codes come through registers), so nothing else is in flight.
@@ -39,8 +41,9 @@ constexpr int HPC = 64, HQ = 128;       // heads per CTA, per cluster
 constexpr int DQK = 576, DV = 512;
 constexpr int KCH = DQK / 64;           // 9 column chunks of 64
 constexpr int TILE = 128;
+constexpr int KG = 3, KPG = KCH / KG;    // K in three groups of three chunks
 constexpr int INFO = 4;                 // row-mask ring
-constexpr int THREADS = 512;
+constexpr int THREADS = 768, DEQ = 8;    // DEQ: warps of each dequantising group
 constexpr int ROW_CODE = DQK / 2, ROW_SCALE = DQK / 16;      // 288, 36 bytes
 
 constexpr uint32_t TM_S = 0;            // S buffers at 0 and 64
@@ -52,15 +55,17 @@ struct __align__(1024) Smem {
     uint8_t k[KCH][64 * 128];           // [chunk][64 rows][64 columns], K-major
     uint8_t v[2][2][TILE * 128];        // [value block j][atom][128 rows][64 columns], MN-major
     uint8_t p[2][HPC * 128];            // [unit][64 heads][64 rows], K-major
-    uint64_t k_full, v_full, p_full;    // the even CTA's: 8, 8 and 2 arrivals
-    uint64_t s_full[2], s_empty[2];     // s_full[u & 1]: Q K^T of tile u done (K may be rewritten)
-    uint64_t pv_done[2];                // pv_done[u & 1]: P V of tile u done (V and P may be rewritten)
+    uint64_t k_full;                    // the even CTA's, 16 arrivals (one a warp): K is written
+    uint64_t k_empty[KG];               // the MMAs that read that part of K are done
+    uint64_t pv_full[2];                // the even CTA's, 16 arrivals: V and P of unit a of the tile are written
+    uint64_t pv_done[2];                // P V over unit a is done: its V and P may be rewritten
+    uint64_t s_full[2];                 // S buffers
     uint64_t info_full[INFO];
     uint64_t mma_done;
     uint64_t never;                     // no arrival ever: the failure-path test's wait
-    uint32_t mask[INFO][4];             // present rows of a tile
+    alignas(16) uint16_t mask[INFO][DEQ];           // present rows of a tile, 16 a word
     float qmul[HPC];                    // per head: score factor, scale * log2(e) * k_scale * 2^e
-    float red[128];
+    float red[2][128];                  // row maxima of the two units, by u & 1
     uint32_t tmem_base;
     int abort_flag;
 };
@@ -73,17 +78,44 @@ __device__ __noinline__ void set_abort(Smem &sm, int32_t *status) {
     flag(status, LSA_DEV_TIMEOUT);
 }
 
-// Warp-uniform bounded wait (lane 0 polls, result broadcast).
-template <bool CLUSTER>
-__device__ __forceinline__ bool warp_wait(Smem &sm, const uint64_t *bar, uint32_t parity, int32_t *status,
-                                          uint64_t limit = WAIT_NS) {
-    bool ok = true;
-    if ((threadIdx.x & 31) == 0) {
-        volatile int *abort = &sm.abort_flag;
-        ok = *abort == 0 && (CLUSTER ? mbar_wait_cluster(bar, parity, limit, abort) : mbar_wait(bar, parity, limit, abort));
-        if (!ok && *abort == 0) set_abort(sm, status);
+// Bounded wait on the SM's own clock: reading the global timer between two tries takes longer than most
+// of these waits last.  The limit is some two seconds of cycles; the abort flag is looked at after 2^18.
+constexpr long long WAIT_CYCLES = 1ll << 32, STALL_CYCLES = 1ll << 22, ABORT_CYCLES = 1ll << 18;
+__device__ __noinline__ bool wait_longer(uint32_t a, uint32_t parity, const volatile int *abort, long long limit) {
+    const long long t0 = clock64();
+    for (;;) {
+        if (mbar_try_wait(a, parity)) return true;
+        const long long dt = clock64() - t0;
+        if (dt > limit || (dt > ABORT_CYCLES && *abort)) return false;
     }
-    return __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+}
+__device__ __forceinline__ bool wait_for(const uint64_t *bar, uint32_t parity, const volatile int *abort,
+                                         long long limit = WAIT_CYCLES) {
+    const uint32_t a = smem_addr(bar);
+    return mbar_try_wait(a, parity) || wait_longer(a, parity, abort, limit);
+}
+
+// Bounded wait of a whole warp (every lane polls the same word, so that the usual case, a phase that is
+// complete already, is one shared-memory access and no exchange).  Operands in shared memory are
+// written by generic stores, each writer's followed by its own fence.proxy.async before the arrive.
+__device__ __forceinline__ bool warp_wait(Smem &sm, const uint64_t *bar, uint32_t parity, int32_t *status,
+                                          long long limit = WAIT_CYCLES) {
+    volatile int *abort = &sm.abort_flag;
+    const bool ok = __all_sync(0xffffffffu, wait_for(bar, parity, abort, limit));
+    if (!ok && *abort == 0) set_abort(sm, status);
+    return ok;
+}
+
+// One lane of a converged warp (always the same one), by the instruction that says so: the compiler then
+// knows that the branch is taken by one lane and keeps the MMA descriptors in uniform registers.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t pred;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}\n"
+        : "=r"(pred));
+    return pred != 0;
 }
 
 __host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, bool b_mn_major) {
@@ -91,19 +123,18 @@ __host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, bool b_mn_maj
            (uint32_t(M >> 4) << 24);
 }
 
-// 32 codes (two groups) with their two scale bytes -> four 16-byte units of eight f16 values at
-// units first .. first + 3 of a 128-byte swizzled row.
-__device__ __forceinline__ void store_piece(uint32_t row_addr, int row, int first, const uint4 &c, uint32_t scales) {
-    const uint32_t f = q4::e4m3x2_to_f16(scales), s[2] = {q4::dup_lo(f), q4::dup_hi(f)};
-    const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+// The 16 codes of one group with their scale byte -> two 16-byte units of eight f16 values, at the
+// addresses row + off0 and row + off1 (the swizzled places of two neighbouring units).
+__device__ __forceinline__ void store_group(uint32_t row, uint32_t off0, uint32_t off1, const uint2 &c, uint32_t scale) {
+    const uint32_t s = q4::dup_lo(q4::e4m3x2_to_f16(scale));
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 2; ++i) {
         uint32_t h[4];
-        q4::e2m1x8_to_f16(w[i], h);
+        q4::e2m1x8_to_f16(i ? c.y : c.x, h);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) h[j] = q4::hmul2(h[j], s[i >> 1]);
-        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(row_addr + (((first + i) ^ (row & 7)) << 4)),
-                     "r"(h[0]), "r"(h[1]), "r"(h[2]), "r"(h[3])
+        for (int j = 0; j < 4; ++j) h[j] = q4::hmul2(h[j], s);
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(row + (i ? off1 : off0)), "r"(h[0]), "r"(h[1]),
+                     "r"(h[2]), "r"(h[3])
                      : "memory");
     }
 }
@@ -114,26 +145,46 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
-// Pool row of row i of unit u, -1 if absent (past the set, or without a slot).
-__device__ __forceinline__ int64_t unit_row(const Units &un, const DecodeParams &p, int b, int u, int i) {
-    if (u >= un.total) return -1;
-    if (u < un.t_topk) return un.topk_row(p, b, u, i);
-    if (!un.in_window(u, i)) return -1;
-    const int slot = un.window_slot(p, b, u);
-    return slot < 0 ? -1 : (int64_t)slot * LSA_CHUNK + i;
+// The row lookup is two dependent loads (position, slot), each issued a tile ahead of its use and
+// checked only then, so that no warp stands still for it.
+// Position of row i of unit u; ABSENT past the set.
+constexpr int ABSENT = INT32_MIN;
+__device__ __forceinline__ int row_position(const Units &un, const DecodeParams &p, int b, int u, int i) {
+    if (u >= un.total) return ABSENT;
+    if (u < un.t_topk) {
+        const int r = u * LSA_CHUNK + i;
+        return r < un.tk ? __ldg(p.topk_idx + (size_t)b * p.k + r) : ABSENT;
+    }
+    return un.in_window(u, i) ? (un.first_chunk + (u - un.t_topk)) * LSA_CHUNK + i : ABSENT;
+}
+// Table entry of a position, -1 if it has none.
+__device__ __forceinline__ int row_slot(const DecodeParams &p, int b, int pos) {
+    return pos >= 0 && pos / LSA_CHUNK < p.table_stride ? __ldg(p.table + (size_t)b * p.table_stride + pos / LSA_CHUNK) : -1;
+}
+// Pool row from both, -1 if the row takes no part (flagged unless it is past the set).
+__device__ __forceinline__ int64_t pool_row(const DecodeParams &p, int pos, int slot) {
+    if (slot >= 0 && slot < p.n_slots) return (int64_t)slot * LSA_CHUNK + (pos & (LSA_CHUNK - 1));
+    if (pos != ABSENT) flag(p.status, pos < 0 ? LSA_DEV_INDEX : LSA_DEV_TABLE);
+    return -1;
 }
 
-// Reads piece `piece` (32 codes) of a row and its two scales.
-__device__ __forceinline__ void load_piece(const uint8_t *pool, int64_t row, int piece, uint4 &c, uint32_t &s) {
-    c = make_uint4(0, 0, 0, 0);
-    s = 0;
-    if (row >= 0) {
-        const uint8_t *chunk = pool + (row >> 6) * q4::chunk_bytes(DQK);
-        const int r = (int)(row & 63);
-        c = __ldg(reinterpret_cast<const uint4 *>(chunk + r * ROW_CODE + piece * 16));
-        s = __ldg(reinterpret_cast<const uint16_t *>(chunk + LSA_CHUNK * ROW_CODE + r * ROW_SCALE + piece * 2));
+// A lane's place in a pool row: its group of 16 in every 64 columns.  An absent row reads the
+// pool's first row and gets zero scales, which make it zeros whatever it holds.
+struct RowPtr {
+    const uint8_t *code, *scale;
+    bool there;
+    __device__ RowPtr(const uint8_t *pool, int64_t row, int quarter) {
+        there = row >= 0;
+        const uint8_t *chunk = pool + (there ? row >> 6 : 0) * q4::chunk_bytes(DQK);
+        const int r = there ? (int)(row & 63) : 0;
+        code = chunk + r * ROW_CODE + quarter * 8;
+        scale = chunk + LSA_CHUNK * ROW_CODE + r * ROW_SCALE + quarter;
     }
-}
+    __device__ __forceinline__ void load(int chunk, uint2 &c, uint32_t &s) const {
+        c = __ldg(reinterpret_cast<const uint2 *>(code + 32 * chunk));
+        s = there ? (uint32_t)__ldg(scale + 4 * chunk) : 0u;
+    }
+};
 
 __global__ void __launch_bounds__(THREADS, 1) q4_mla_kernel(const DecodeParams p, int stall) {
     extern __shared__ uint8_t smem_raw[];
@@ -147,32 +198,84 @@ __global__ void __launch_bounds__(THREADS, 1) q4_mla_kernel(const DecodeParams p
     auto tile_of = [&](int u) { return split + u * p.n_splits; };
 
     if (threadIdx.x == 0) {
-        mbar_init(&sm.k_full, 8);
-        mbar_init(&sm.v_full, 8);
-        mbar_init(&sm.p_full, 2);
-        for (int i = 0; i < 2; ++i) { mbar_init(&sm.s_full[i], 1); mbar_init(&sm.s_empty[i], 2); mbar_init(&sm.pv_done[i], 1); }
-        for (int i = 0; i < INFO; ++i) mbar_init(&sm.info_full[i], 4);
-        mbar_init(&sm.mma_done, 2);   // one commit from each MMA issuer
+        mbar_init(&sm.k_full, 2 * DEQ);
+        for (int i = 0; i < KG; ++i) mbar_init(&sm.k_empty[i], 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sm.pv_full[i], DEQ + 8);
+            mbar_init(&sm.pv_done[i], 1);
+            mbar_init(&sm.s_full[i], 1);
+        }
+        for (int i = 0; i < INFO; ++i) mbar_init(&sm.info_full[i], DEQ);
+        mbar_init(&sm.mma_done, 1);
         mbar_init(&sm.never, 1);
         sm.abort_flag = 0;
         fence_mbar_init_cluster();
     }
     if (warp == 2) tmem_alloc_pair(&sm.tmem_base, TM_COLS);
+    // ---- the dequantising warps look up and load their part of the first tile
+    // K: unit `rank` of each tile, 8 rows a warp, all nine column chunks.  V: all rows of the tile, 16 a warp
+    // in two passes of 8, this CTA's four chunks.  Four lanes share a row, each takes 16 columns of
+    // a chunk, so that the shared stores of eight lanes touch all banks.  Lane i looks up row i of the warp's.
+    const bool kwarp = warp >= 8 && warp < 16, vwarp = warp >= 16;
+    const int w = warp & 7, quarter = lane & 3;
+    const int unit_in_tile = kwarp ? (int)rank : w >> 2, first_row = kwarp ? 8 * w : 16 * (w & 3);   // in that unit
+    auto position = [&](int u) -> int {
+        return u < n_tiles ? row_position(un, p, b, 2 * tile_of(u) + unit_in_tile, first_row + (lane & (kwarp ? 7 : 15))) : ABSENT;
+    };
+    uint2 c[KCH];
+    uint32_t sc[KCH];
+    int pos1 = ABSENT, pos2 = ABSENT, slot1 = -1;     // of tiles u + 1 and u + 2 in the loops below
+    auto load = [&](int64_t r) {
+        if (kwarp) {
+            const RowPtr row(p.k_pool, __shfl_sync(0xffffffffu, r, lane >> 2), quarter);
+#pragma unroll
+            for (int i = 0; i < KCH; ++i) row.load(i, c[i], sc[i]);
+        } else {
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                const RowPtr row(p.k_pool, __shfl_sync(0xffffffffu, r, 8 * q + (lane >> 2)), quarter);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) row.load(4 * (i >> 1) + 2 * (int)rank + (i & 1), c[2 * i + q], sc[2 * i + q]);
+            }
+        }
+    };
+    // Row presence of tile u for the softmax, posted before this warp writes V of tile u - 1.  The ring slot
+    // was last read for tile u - 4, by softmax warps of the same unit, whose P V was done before this warp
+    // wrote V of tile u - 3.
+    auto post_mask = [&](int u, int64_t r) {
+        const uint32_t m = __ballot_sync(0xffffffffu, r >= 0);
+        if (lane == 0) {
+            sm.mask[u % INFO][w] = (uint16_t)m;
+            asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];\n" ::"r"(smem_addr(&sm.info_full[u % INFO])) : "memory");
+        }
+        __syncwarp();
+    };
+    int64_t row0 = -1;
+    if (warp >= 8 && n_tiles > 0) {
+        const int pos0 = position(0);
+        pos1 = position(1);
+        pos2 = position(2);
+        const int slot0 = row_slot(p, b, pos0);
+        slot1 = row_slot(p, b, pos1);
+        row0 = pool_row(p, pos0, slot0);
+        load(row0);
+    }
     if (n_tiles > 0) {
-        // queries as f16 over a power of two, straight into the operand layout
+        // ---- queries as f16 over a power of two, straight into the operand layout
         const uint32_t qb = smem_addr(sm.q);
+#pragma unroll 1
         for (int h = warp; h < HPC; h += THREADS / 32) {
             const int head = HPC * (int)rank + h;
-            const bool live = head < p.Hq;
-            const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.q) +
-                                                               ((size_t)b * p.Hq + (live ? head : 0)) * DQK);
+            const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.q) + ((size_t)b * p.Hq + head) * DQK);
+            uint4 raw[3];
+#pragma unroll
+            for (int i = 0; i < 3; ++i)
+                raw[i] = head < p.Hq && lane + 32 * i < DQK / 8 ? __ldg(src + lane + 32 * i) : make_uint4(0, 0, 0, 0);
             float x[3][8];
             float amax = 0.f;
 #pragma unroll
             for (int i = 0; i < 3; ++i) {
-                const int piece = lane + 32 * i;
-                const uint4 w = live && piece < DQK / 8 ? __ldg(src + piece) : make_uint4(0, 0, 0, 0);
-                const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+                const uint32_t ww[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     if (p.q_f16) {
@@ -188,7 +291,7 @@ __global__ void __launch_bounds__(THREADS, 1) q4_mla_kernel(const DecodeParams p
             amax = warp_max(amax);
             float inv;
             const float e = q4::row_exponent(amax, inv);
-            if (lane == 0) sm.qmul[h] = e * p.scale_log2;
+            if (lane == 0) sm.qmul[h] = fmaxf(e * p.scale_log2, 1.2e-38f);   // not 0: 0 * -inf is NaN
 #pragma unroll
             for (int i = 0; i < 3; ++i) {
                 const int piece = lane + 32 * i;
@@ -209,126 +312,102 @@ __global__ void __launch_bounds__(THREADS, 1) q4_mla_kernel(const DecodeParams p
     const uint32_t tmem = sm.tmem_base;
 
     if (warp == 0 && rank == 0 && n_tiles > 0) {
-        // ------------------------------------------------ S = Q K^T issuer
-        constexpr uint32_t IDESC = idesc_f16_f32(HQ, TILE, false);
+        // ------------------------------------------------ MMA issuer: S(0), then S(u + 1) and O += P V(u) in turn
+        constexpr uint32_t IDESC_QK = idesc_f16_f32(HQ, TILE, false), IDESC_PV = idesc_f16_f32(HQ, 256, true);
         constexpr uint64_t CHUNK = (64 * 128) >> 4, K16 = 32 >> 4;
+        constexpr uint64_t P_ATOM = (HPC * 128) >> 4, V_J = (2 * TILE * 128) >> 4, V16 = (16 * 128) >> 4;
         const uint64_t qd = smem_desc_sw128(smem_addr(sm.q), 16, 1024), kd = smem_desc_sw128(smem_addr(sm.k), 16, 1024);
+        const uint64_t pd = smem_desc_sw128(smem_addr(sm.p), 16, 1024), vd = smem_desc_sw128(smem_addr(sm.v), TILE * 128, 1024);
         bool ok = true;
-        if (stall) ok = warp_wait<false>(sm, &sm.never, 0, p.status, TEST_STALL_NS);
-        for (int u = 0; u < n_tiles && ok; ++u) {
-            const int sb = u & 1;
-            ok = warp_wait<true>(sm, &sm.s_empty[sb], ((u >> 1) + 1) & 1, p.status) &&
-                 warp_wait<true>(sm, &sm.k_full, u & 1, p.status);
-            if (!ok) break;
-            tc_fence_after();
-            if (lane == 0) {
+        if (stall) ok = warp_wait(sm, &sm.never, 0, p.status, STALL_CYCLES);
+#pragma unroll 1
+        for (int u = -1; u < n_tiles && ok; ++u) {
+            // The S buffer of tile u + 1 was read before P of tile u - 1 was written, which P V(u - 1) waited for.
+            const int n = u + 1, sb = n & 1;
+            if (n < n_tiles) {
+                ok = warp_wait(sm, &sm.k_full, n & 1, p.status);
+                if (!ok) break;
+                tc_fence_after();
+                if (elect_one()) {
+#pragma unroll 1
+                    for (int g = 0; g < KG; ++g) {
+#pragma unroll 1
+                        for (int c = KPG * g; c < KPG * (g + 1); ++c) {
+                            const uint64_t at = CHUNK * c;
 #pragma unroll
-                for (int c = 0; c < KCH; ++c)
-#pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)
-                        umma_pair_ss(tmem + TM_S + 64 * sb, qd + CHUNK * c + K16 * kk, kd + CHUNK * c + K16 * kk, IDESC,
-                                     (c | kk) != 0);
-                umma_commit_pair(&sm.s_full[sb], 0x3);
+                            for (int kk = 0; kk < 4; ++kk)
+                                umma_pair_ss(tmem + TM_S + 64 * sb, qd + at + K16 * kk, kd + at + K16 * kk, IDESC_QK, (c | kk) != 0);
+                        }
+                        umma_commit_pair(&sm.k_empty[g], 0x3);
+                    }
+                    umma_commit_pair(&sm.s_full[sb], 0x3);
+                }
+                __syncwarp();
             }
-            __syncwarp();
-        }
-        if (lane == 0) umma_commit_pair(&sm.mma_done, 0x3);
-        __syncwarp();
-    } else if (warp == 1 && rank == 0 && n_tiles > 0) {
-        // ------------------------------------------------ O += P V issuer
-        constexpr uint32_t IDESC = idesc_f16_f32(HQ, 256, true);
-        constexpr uint64_t P_ATOM = (HPC * 128) >> 4, V_J = (2 * TILE * 128) >> 4, V16 = (16 * 128) >> 4, K16 = 32 >> 4;
-        const uint64_t pd = smem_desc_sw128(smem_addr(sm.p), 16, 1024);
-        const uint64_t vd = smem_desc_sw128(smem_addr(sm.v), TILE * 128, 1024);
-        bool ok = true;
-        for (int u = 0; u < n_tiles && ok; ++u) {
-            ok = warp_wait<true>(sm, &sm.p_full, u & 1, p.status) && warp_wait<true>(sm, &sm.v_full, u & 1, p.status);
-            if (!ok) break;
-            tc_fence_after();
-            if (lane == 0) {
+#pragma unroll 1
+            for (int a = 0; a < 2 && u >= 0; ++a) {
+                ok = warp_wait(sm, &sm.pv_full[a], u & 1, p.status);
+                if (!ok) break;
+                tc_fence_after();
+                if (elect_one()) {
+#pragma unroll 1
+                    for (int j = 0; j < 2; ++j)
 #pragma unroll
-                for (int j = 0; j < 2; ++j)
-#pragma unroll
-                    for (int kk = 0; kk < 8; ++kk)
-                        umma_pair_ss(tmem + TM_O + 128 * j, pd + P_ATOM * (kk >> 2) + K16 * (kk & 3), vd + V_J * j + V16 * kk,
-                                     IDESC, u > 0 || kk > 0);
-                umma_commit_pair(&sm.pv_done[u & 1], 0x3);
+                        for (int kk = 0; kk < 4; ++kk)
+                            umma_pair_ss(tmem + TM_O + 128 * j, pd + P_ATOM * a + K16 * kk, vd + V_J * j + V16 * (4 * a + kk), IDESC_PV,
+                                         (u | a | kk) != 0);
+                    umma_commit_pair(&sm.pv_done[a], 0x3);
+                }
+                __syncwarp();
             }
-            __syncwarp();
         }
-        if (lane == 0) umma_commit_pair(&sm.mma_done, 0x3);
+        if (elect_one()) umma_commit_pair(&sm.mma_done, 0x3);
         __syncwarp();
-    } else if (warp >= 8 && warp < 12 && n_tiles > 0) {
-        // ------------------------------------------------ K: unit `rank` of each tile, 16 rows a warp
-        const int w = warp - 8, row = 16 * w + (lane >> 1), hf = lane & 1;
+    } else if (kwarp && n_tiles > 0) {
+        // ------------------------------------------------ dequantise K
+        const int row = first_row + (lane >> 2);
         const uint32_t dst = smem_addr(sm.k) + row * 128, full = map_to_rank(&sm.k_full, 0);
-        auto resolve = [&](int u) -> int64_t {
-            return u < n_tiles ? unit_row(un, p, b, 2 * tile_of(u) + (int)rank, row) : -1;
-        };
-        uint4 c[KCH];
-        uint32_t s[KCH];
-        int64_t r = resolve(0);
+        const uint32_t off0 = ((2 * quarter) ^ (row & 7)) << 4, off1 = off0 ^ 16;
+        bool ok = true;
+        for (int u = 0; u < n_tiles && ok; ++u) {
 #pragma unroll
-        for (int i = 0; i < KCH; ++i) load_piece(p.k_pool, r, 2 * i + hf, c[i], s[i]);
-        r = resolve(1);
-        for (int u = 0; u < n_tiles; ++u) {
-            if (u > 0 && !warp_wait<false>(sm, &sm.s_full[(u - 1) & 1], ((u - 1) >> 1) & 1, p.status)) break;
+            for (int g = 0; g < KG; ++g) {
+                if (u > 0) ok = ok && warp_wait(sm, &sm.k_empty[g], (u - 1) & 1, p.status);
+                if (!ok) break;
 #pragma unroll
-            for (int i = 0; i < KCH; ++i) store_piece(dst + i * (64 * 128), row, 4 * hf, c[i], s[i]);
+                for (int i = KPG * g; i < KPG * (g + 1); ++i) store_group(dst + i * (64 * 128), off0, off1, c[i], sc[i]);
+            }
+            if (!ok) break;
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) mbar_arrive_release_cluster(full);
-#pragma unroll
-            for (int i = 0; i < KCH; ++i) load_piece(p.k_pool, r, 2 * i + hf, c[i], s[i]);
-            r = resolve(u + 2);
+            if (lane == 0) mbar_arrive_cluster(full);
+            load(pool_row(p, pos1, slot1));
+            slot1 = row_slot(p, b, pos2);
+            pos1 = pos2;
+            pos2 = position(u + 3);
         }
-    } else if (warp >= 12 && n_tiles > 0) {
-        // ------------------------------------------------ V: all rows of the tile, this CTA's columns, 32 rows a warp
-        const int w = warp - 12, hf = lane & 1;
-        const uint32_t vb = smem_addr(sm.v), full = map_to_rank(&sm.v_full, 0);
-        // lane i looks up row 32 w + i of the tile, whose presence the softmax needs
-        auto resolve = [&](int u) -> int64_t {
-            if (u >= n_tiles) return -1;
-            const int i = 32 * w + lane;
-            const int64_t r = unit_row(un, p, b, 2 * tile_of(u) + (i >> 6), i & 63);
-            const uint32_t m = __ballot_sync(0xffffffffu, r >= 0);
-            // The ring slot was last read for tile u - 4; P V of tile u - 3 was done before
-            // this warp wrote V of tile u - 2, so that read is long past.
-            if (lane == 0) {
-                sm.mask[u % INFO][w] = m;
-                asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];\n" ::"r"(smem_addr(&sm.info_full[u % INFO])) : "memory");
-            }
-            __syncwarp();
-            return r;
-        };
-        uint4 c[8];
-        uint32_t s[8];
-        auto load = [&](int64_t r) {
+    } else if (vwarp && n_tiles > 0) {
+        // ------------------------------------------------ dequantise V, post the row masks
+        const int row = 16 * w + (lane >> 2);
+        const uint32_t dst = smem_addr(sm.v) + row * 128, full = map_to_rank(&sm.pv_full[w >> 2], 0);
+        const uint32_t off0 = ((2 * quarter) ^ (row & 7)) << 4, off1 = off0 ^ 16;
+        bool ok = true;
+        post_mask(0, row0);
+        for (int u = 0; u < n_tiles && ok; ++u) {
+            const int64_t next = pool_row(p, pos1, slot1);
+            if (u + 1 < n_tiles) post_mask(u + 1, next);
+            if (u > 0) ok = warp_wait(sm, &sm.pv_done[w >> 2], (u - 1) & 1, p.status);
+            if (!ok) break;
 #pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                const int64_t rr = __shfl_sync(0xffffffffu, r, 16 * q + (lane >> 1));
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    load_piece(p.k_pool, rr, 2 * (4 * (i >> 1) + 2 * (int)rank + (i & 1)) + hf, c[4 * q + i], s[4 * q + i]);
-            }
-        };
-        int64_t r = resolve(0);
-        load(r);
-        r = resolve(1);
-        for (int u = 0; u < n_tiles; ++u) {
-            if (u > 0 && !warp_wait<false>(sm, &sm.pv_done[(u - 1) & 1], ((u - 1) >> 1) & 1, p.status)) break;
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                const int row = 32 * w + 16 * q + (lane >> 1);
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    store_piece(vb + i * (TILE * 128) + row * 128, row, 4 * hf, c[4 * q + i], s[4 * q + i]);
-            }
+            for (int i = 0; i < 8; ++i)       // chunk i >> 1, rows row and row + 8
+                store_group(dst + (i >> 1) * (TILE * 128) + (i & 1) * 1024, off0, off1, c[i], sc[i]);
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) mbar_arrive_release_cluster(full);
-            load(r);
-            r = resolve(u + 2);
+            if (lane == 0) mbar_arrive_cluster(full);
+            load(next);
+            slot1 = row_slot(p, b, pos2);
+            pos1 = pos2;
+            pos2 = position(u + 3);
         }
     } else if (warp >= 4 && warp < 8) {
         // ------------------------------------------------ softmax + epilogue
@@ -341,54 +420,54 @@ __global__ void __launch_bounds__(THREADS, 1) q4_mla_kernel(const DecodeParams p
         for (int u = 0; u < n_tiles; ++u) {
             const int s = u & 1;
             ok = ok && *(volatile int *)&sm.abort_flag == 0;
-            if (ok) ok = mbar_wait(&sm.info_full[u % INFO], (u / INFO) & 1, WAIT_NS, &sm.abort_flag);
+            if (ok) ok = wait_for(&sm.info_full[u % INFO], (u / INFO) & 1, &sm.abort_flag);
             uint32_t vm[2] = {0u, 0u};
-            if (ok) { vm[0] = sm.mask[u % INFO][2 * half]; vm[1] = sm.mask[u % INFO][2 * half + 1]; }
-            if (ok) ok = mbar_wait(&sm.s_full[s], (u >> 1) & 1, WAIT_NS, &sm.abort_flag);
+            if (ok) {
+                const uint32_t *m = reinterpret_cast<const uint32_t *>(&sm.mask[u % INFO][4 * half]);
+                vm[0] = m[0];
+                vm[1] = m[1];
+            }
+            if (ok) ok = wait_for(&sm.s_full[s], (u >> 1) & 1, &sm.abort_flag);
             if (!ok && *(volatile int *)&sm.abort_flag == 0) set_abort(sm, p.status);
             tc_fence_after();
-            uint32_t raw[2][32];
-            tmem_ld32(tmem + lane_base + TM_S + 64 * s, raw[0]);
-            tmem_ld32(tmem + lane_base + TM_S + 64 * s + 32, raw[1]);
-            tmem_wait_ld();
-            tc_fence_before();
-            float mx = -INFINITY;
+            // Two passes over S (maximum, then weights), 32 columns at a time: 64 scores at once
+            // would not fit the registers of 24 warps.  The factor is positive, so the
+            // maximum of the raw products is the scores'.
+            uint32_t raw[32];
+            auto fetch = [&](int q) {
+                tmem_ld32(tmem + lane_base + TM_S + 64 * s + 32 * q, raw);
+                tmem_wait_ld();
+                if (vm[q] != 0xffffffffu) {      // uniform over the warp: absent rows in this unit
 #pragma unroll
-            for (int q = 0; q < 2; ++q)
-#pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                    const float x = (vm[q] >> i) & 1u ? __uint_as_float(raw[q][i]) * mul : -INFINITY;
-                    raw[q][i] = __float_as_uint(x);
-                    mx = fmaxf(mx, x);
+                    for (int i = 0; i < 32; ++i)
+                        if (!((vm[q] >> i) & 1u)) raw[i] = 0xff800000u;
                 }
-            sm.red[L] = mx;
+            };
+            float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll 1
+            for (int q = 0; q < 2; ++q) {
+                fetch(q);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) mx4[i & 3] = fmaxf(mx4[i & 3], __uint_as_float(raw[i]));
+            }
+            float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * mul;
+            sm.red[u & 1][L] = mx;
             named_barrier(1, 128);
-            if (L == 0) mbar_arrive_release_cluster(map_to_rank(&sm.s_empty[s], 0));
-            mx = fmaxf(mx, sm.red[L ^ 64]);
+            mx = fmaxf(mx, sm.red[u & 1][L ^ 64]);
             const bool move = mx > m_ref + q4::RESCALE;
             const float alpha = move ? ex2(m_ref - mx) : 1.f;      // 0 the first time (m_ref = -inf)
             if (move) {
                 l *= alpha;
                 m_ref = mx;
             }
-            const float ref = m_ref == -INFINITY ? 0.f : m_ref - q4::P_SHIFT;
-            float psum = 0.f;
-            uint32_t pk[32];
-#pragma unroll
-            for (int i = 0; i < 32; ++i) {
-                const float p0 = ex2(__uint_as_float(raw[i >> 4][2 * (i & 15)]) - ref);
-                const float p1 = ex2(__uint_as_float(raw[i >> 4][2 * (i & 15) + 1]) - ref);
-                psum += p0 + p1;
-                pk[i] = q4::pack_f16x2(p0, p1);
-            }
-            l += psum;
-            // P is rewritten and O may be rescaled: P V of tile u - 1 must be done
-            if (u > 0 && ok) {
-                ok = mbar_wait(&sm.pv_done[(u - 1) & 1], ((u - 1) >> 1) & 1, WAIT_NS, &sm.abort_flag);
-                if (!ok && *(volatile int *)&sm.abort_flag == 0) set_abort(sm, p.status);
-            }
-            // tcgen05.ld / st are warp-collective: the whole warp rescales when any row moves
+            // O may only be rescaled once both units' P V of tile u - 1 are done.  tcgen05.ld / st are
+            // warp-collective: the whole warp rescales when any of its rows moves.
             if (__any_sync(0xffffffffu, move) && u > 0) {
+#pragma unroll 1
+                for (int a = 0; a < 2; ++a) {
+                    ok = ok && wait_for(&sm.pv_done[a], (u - 1) & 1, &sm.abort_flag);
+                    if (!ok && *(volatile int *)&sm.abort_flag == 0) set_abort(sm, p.status);
+                }
                 tc_fence_after();
 #pragma unroll 1
                 for (int q = 0; q < 8; ++q) {
@@ -400,27 +479,61 @@ __global__ void __launch_bounds__(THREADS, 1) q4_mla_kernel(const DecodeParams p
                     tmem_st32(tmem + lane_base + TM_O + 32 * q, o);
                 }
                 tmem_wait_st();
+                tc_fence_before();
             }
+            const float ref = m_ref == -INFINITY ? 0.f : m_ref - q4::P_SHIFT;
+            // P V of tile u over the other unit needs this warp's lanes of O rescaled, though not its P, so
+            // the warp arrives for that unit too -- once P V of tile u - 1 over it is done: only then has the
+            // barrier's phase of tile u begun (the peer CTA may be a tile behind).
+            auto done = [&](int a) {
+                if (ok) ok = wait_for(&sm.pv_done[a], (u - 1) & 1, &sm.abort_flag);
+                if (!ok && *(volatile int *)&sm.abort_flag == 0) set_abort(sm, p.status);
+            };
+            auto turn = [&](int a) {
+                if (u > 0) done(a);
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(map_to_rank(&sm.pv_full[a], 0));
+            };
+            float psum[4] = {0.f, 0.f, 0.f, 0.f};
             uint8_t *prow = sm.p[half] + h * 128;
+#pragma unroll 1
+            for (int q = 0; q < 2; ++q) {
+                fetch(q);
+                uint32_t pk[16];
 #pragma unroll
-            for (int c = 0; c < 8; ++c)
-                *reinterpret_cast<uint4 *>(prow + ((c ^ (h & 7)) << 4)) =
-                    make_uint4(pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
-            fence_proxy_async_smem();
+                for (int i = 0; i < 16; ++i) {
+                    const float p0 = ex2(fmaf(__uint_as_float(raw[2 * i]), mul, -ref));
+                    const float p1 = ex2(fmaf(__uint_as_float(raw[2 * i + 1]), mul, -ref));
+                    psum[i & 3] += p0 + p1;
+                    pk[i] = q4::pack_f16x2(p0, p1);
+                }
+                if (q == 0) {
+                    if (half == 1) turn(0);
+                    if (u > 0) done(half);         // P of this unit is rewritten
+                }
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    *reinterpret_cast<uint4 *>(prow + (((4 * q + c) ^ (h & 7)) << 4)) =
+                        make_uint4(pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
+            }
+            l += (psum[0] + psum[1]) + (psum[2] + psum[3]);
             tc_fence_before();
-            named_barrier(1, 128);
-            if (L == 0) mbar_arrive_release_cluster(map_to_rank(&sm.p_full, 0));
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(map_to_rank(&sm.pv_full[half], 0));
+            if (half == 0) turn(1);
         }
         // ---- epilogue: wait for the last P V, then write the partial
-        if (n_tiles > 0 && ok) {
-            ok = mbar_wait(&sm.pv_done[(n_tiles - 1) & 1], ((n_tiles - 1) >> 1) & 1, WAIT_NS, &sm.abort_flag);
+#pragma unroll 1
+        for (int a = 0; a < 2 && n_tiles > 0 && ok; ++a) {
+            ok = wait_for(&sm.pv_done[a], (n_tiles - 1) & 1, &sm.abort_flag);
             if (!ok && *(volatile int *)&sm.abort_flag == 0) set_abort(sm, p.status);
         }
         tc_fence_after();
         named_barrier(1, 128);
-        sm.red[L] = l;
+        sm.red[0][L] = l;
         named_barrier(1, 128);
-        const float l_tot = l + sm.red[L ^ 64];
+        const float l_tot = l + sm.red[0][L ^ 64];
         const int head = HPC * (int)rank + h;
         const size_t part0 = ((size_t)b * p.n_splits + split) * p.Hq;
         if (half == 0 && head < p.Hq) {
