@@ -6,6 +6,7 @@
 #include <cuda_bf16.h>
 #include <stdint.h>
 #include <stdio.h>
+#include <atomic>
 #include <string>
 
 #include "../../include/lsa.h"
@@ -46,6 +47,18 @@ int take_test_stall(int which);
 
 __host__ __device__ inline int64_t lsa_min64(int64_t a, int64_t b) { return a < b ? a : b; }
 __host__ __device__ inline int64_t lsa_max64(int64_t a, int64_t b) { return a > b ? a : b; }
+
+// Raises a kernel's dynamic shared memory limit, once per device and kernel (`done`: one bit a device).
+template <class K>
+int allow_shared(K kernel, int bytes, std::atomic<uint64_t> &done) {
+    int dev = 0;
+    LSA_CUDA(cudaGetDevice(&dev));
+    const uint64_t bit = 1ull << (dev & 63);
+    if (done.load(std::memory_order_relaxed) & bit) return LSA_OK;
+    LSA_CUDA(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes));
+    done.fetch_or(bit, std::memory_order_relaxed);
+    return LSA_OK;
+}
 
 inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 

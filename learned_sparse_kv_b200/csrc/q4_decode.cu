@@ -16,8 +16,14 @@
 //    O^T lane group g takes value columns D/8 g .. , contiguous again, and the tokens pair up by
 //    byte permutes of two tokens' f16 pairs.
 //  - P^T goes from the accumulator layout to the operand layout with movmatrix, no memory.
-// A CTA's warps merge through shared memory; CTAs of one (sequence, K/V head) split its units
-// and their partials are merged by a second kernel.
+// The grid is one wave of CTAs.  All units of all (sequence, K/V head, group of query heads) segments are
+// counted on the device and dealt to the CTAs in equal contiguous ranges, so ragged lengths cost
+// nothing: a CTA walks the segments of its range, its warps take a segment's units in turn and merge
+// through shared memory.  A segment counts SETUP units more than it has, which is what its start
+// and its merge take: otherwise one CTA could be dealt all of the shortest sequences (16 sequences of 1 to
+// 16K tokens, 8 K/V heads: 41.6 us without).  A segment that lies inside one range is finished there; the at most two
+// that a CTA shares with others leave partials for a second kernel.
+#include "block_scan.cuh"
 #include "nvtx_range.cuh"
 #include "q4_rows.cuh"
 
@@ -25,11 +31,13 @@ namespace lsa {
 namespace q4 {
 
 constexpr int WARPS = 4;
+constexpr int SETUP = 8;
 
 template <int D_, int NH_>
 struct Cfg {
     static constexpr int D = D_, NH = NH_;          // head width; tiles of 8 query heads
-    static constexpr int STAGES = 3;
+    static constexpr int CTAS = NH == 1 ? 3 : 2;    // a multiprocessor: registers
+    static constexpr int STAGES = NH == 1 ? 2 : 3;
     static constexpr int CODE = D / 2, SCALES = D / 16;   // bytes of a row
     static constexpr int HALF = 64 * (CODE + SCALES);     // one side of one unit: 36 D
     static constexpr int STAGE = 2 * HALF;
@@ -100,23 +108,95 @@ __device__ __forceinline__ uint32_t ld_shared_u8(uint32_t addr) {
     return v;
 }
 
+// Number of units of sequence b (as Units counts them).
+__device__ __forceinline__ int count_units(const DecodeParams &p, int b) {
+    const int tk = p.k > 0 ? min(max(__ldg(p.topk_count + b), 0), p.k) : 0;
+    const int start = __ldg(p.window_start + b);
+    const int len = start < 0 ? 0 : min(max(__ldg(p.window_len + b), 0), INT32_MAX - 63 - start);
+    return (tk + LSA_CHUNK - 1) / LSA_CHUNK + (len > 0 ? (start + len - 1) / LSA_CHUNK - start / LSA_CHUNK + 1 : 0);
+}
+
+template <class T>
+__device__ __forceinline__ void store_out4(void *out, size_t at, const float4 &v) {
+    Vec<T, 4> o;
+    o.v[0] = from_f32<T>(v.x); o.v[1] = from_f32<T>(v.y); o.v[2] = from_f32<T>(v.z); o.v[3] = from_f32<T>(v.w);
+    *reinterpret_cast<Vec<T, 4> *>(static_cast<T *>(out) + at) = o;
+}
+// Four output values at element `at` (a multiple of 4) of out, in its type.
+__device__ __forceinline__ void store_out(const DecodeParams &p, size_t at, const float4 &v) {
+    if (p.out_dtype == LSA_DTYPE_BF16) store_out4<__nv_bfloat16>(p.out, at, v);
+    else if (p.out_dtype == LSA_DTYPE_F16) store_out4<__half>(p.out, at, v);
+    else store_out4<float>(p.out, at, v);
+}
+__device__ __forceinline__ float lse_of(float M, float L) {
+    return L == 0.f ? -INFINITY : (M + log2f(L)) * 0.69314718055994530942f;
+}
+
 template <class C>
-__global__ void __launch_bounds__(WARPS * 32, C::NH == 1 ? 3 : 2) q4_decode_kernel(const DecodeParams p) {
-    constexpr int D = C::D, NH = C::NH;
+__global__ void __launch_bounds__(WARPS * 32, C::CTAS) q4_decode_kernel(const DecodeParams p, int B) {
+    constexpr int D = C::D, NH = C::NH, NT = WARPS * 32;
     extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ int warp_tot[NT / 32 + 1];
+    __shared__ int64_t s_sum[WARPS];
+    __shared__ int s_first_b;
+    __shared__ int64_t s_first_off;
+    __shared__ float sm_m[WARPS][C::HPC], sm_l[WARPS][C::HPC];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const int b = blockIdx.z, split = blockIdx.x;
-    const int G = p.Hq / p.heads, groups = (G + C::HPC - 1) / C::HPC;
-    const int kvh = blockIdx.y / groups, h0 = (blockIdx.y - kvh * groups) * C::HPC;   // first query head of the group
-    const int nh = min(C::HPC, G - h0);                                               // query heads here
-    const size_t qrow0 = (size_t)b * p.Hq + (size_t)kvh * G + h0;
-    const Units un(p, b);
+    const int G = p.Hq / p.heads, groups = (G + C::HPC - 1) / C::HPC, per_seq = p.heads * groups;
+
+    // ---- this CTA's range [lo, hi) of the units of all segments, and the sequence where it begins
+    int64_t total = 0;
+    for (int b = threadIdx.x; b < B; b += NT) {
+        const int n = count_units(p, b);
+        total += n > 0 ? n + SETUP : 0;
+        if (blockIdx.x == 0 && p.window_start[b] < 0 && p.window_len[b] > 0) flag(p.status, LSA_DEV_INDEX);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+    if (lane == 0) s_sum[warp] = total;
+    __syncthreads();
+    total = 0;
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) total += s_sum[w];
+    total *= per_seq;
+    // no more CTAs than give every warp a unit; then no range is empty
+    const int64_t ctas = lsa_min64(gridDim.x, (total + WARPS - 1) / WARPS);
+    if (blockIdx.x >= ctas) return;
+    const int64_t lo = total * blockIdx.x / ctas, hi = total * (blockIdx.x + 1) / ctas;
+    int64_t before = 0;          // units of the sequences before b0
+    for (int b0 = 0; b0 < B; b0 += NT) {
+        const int b = b0 + threadIdx.x;
+        int n = b < B ? count_units(p, b) : 0;
+        if (n > 0) n += SETUP;
+        int tot;
+        const int64_t at = (before + block_exclusive_scan<NT>(n, warp_tot, &tot)) * per_seq;
+        if (n > 0 && at <= lo && lo < at + (int64_t)n * per_seq) { s_first_b = b; s_first_off = at; }
+        before += tot;
+        if (before * per_seq > lo) break;      // uniform
+    }
+    __syncthreads();
+    int b = s_first_b;
+    int64_t seq_at = s_first_off;              // units before sequence b
 
     const uint32_t ring = smem_addr(smem) + warp * C::STAGES * C::STAGE;
     const int64_t slot_stride = p.heads * chunk_bytes(D);
+
+    for (int64_t pos = lo; pos < hi;) {
+    const Units un(p, b);
+    if (un.total == 0) { ++b; continue; }
+    const int cost = un.total + SETUP;
+    const int seg = (int)((pos - seq_at) / cost);                      // K/V head and group
+    const int64_t seg_at = seq_at + (int64_t)seg * cost, seg_end = seg_at + cost;
+    const int kvh = seg / groups, h0 = (seg - kvh * groups) * C::HPC;  // first query head of the group
+    const int nh = min(C::HPC, G - h0);                                // query heads here
+    const size_t qrow0 = (size_t)b * p.Hq + (size_t)kvh * G + h0;
+    const int unit0 = max((int)(pos - seg_at) - SETUP, 0), unit1 = (int)(lsa_min64(seg_end, hi) - seg_at) - SETUP;
+    const bool next_seq = seg == per_seq - 1;
+    pos = lsa_min64(seg_end, hi);
+    if (unit1 <= 0) continue;                // the range ends before the segment's first unit
     const uint8_t *kb = p.k_pool + kvh * chunk_bytes(D), *vb = p.v_pool + kvh * chunk_bytes(D);
-    const int u_first = split * WARPS + warp, u_step = p.n_splits * WARPS;
-    const int n_mine = u_first < un.total ? (un.total - 1 - u_first) / u_step + 1 : 0;
+    const int u_first = unit0 + warp, u_step = WARPS;
+    const int n_mine = u_first < unit1 ? (unit1 - 1 - u_first) / u_step + 1 : 0;
 
     // ---- copies of one unit into a stage; returns this lane's rows (lane, lane + 32) as present
     auto issue = [&](int i) -> uint32_t {
@@ -369,7 +449,6 @@ __global__ void __launch_bounds__(WARPS * 32, C::NH == 1 ? 3 : 2) q4_decode_kern
     cp_async_wait<0>();
 
     // ---- the CTA's warps: M and sum per head, then O through shared memory
-    __shared__ float sm_m[WARPS][C::HPC], sm_l[WARPS][C::HPC];
     __syncthreads();       // every warp is done with its ring
 #pragma unroll
     for (int n = 0; n < NH; ++n)
@@ -393,8 +472,10 @@ __global__ void __launch_bounds__(WARPS * 32, C::NH == 1 ? 3 : 2) q4_decode_kern
             *reinterpret_cast<float2 *>(obuf + (h + 1) * D + col) = make_float2(o[j][n][1], o[j][n][3]);
         }
     __syncthreads();
-    const size_t part0 = ((size_t)b * p.n_splits + split) * p.Hq + (size_t)kvh * G + h0;
-    for (int i = threadIdx.x; i < nh * (D / 4); i += WARPS * 32) {
+    const bool whole = unit0 == 0 && unit1 == un.total;
+    // partials: slot 2c + 1 of CTA c for the segment that begins in its range, slot 2c for one begun before
+    const size_t part0 = (2 * (size_t)blockIdx.x + (unit0 == 0 ? 1 : 0)) * C::HPC;
+    for (int i = threadIdx.x; i < nh * (D / 4); i += NT) {
         const int h = i / (D / 4), c = i % (D / 4);
         float M = -INFINITY;
 #pragma unroll
@@ -408,69 +489,162 @@ __global__ void __launch_bounds__(WARPS * 32, C::NH == 1 ? 3 : 2) q4_decode_kern
             L += f * sm_l[w][h];
             a.x += f * v.x; a.y += f * v.y; a.z += f * v.z; a.w += f * v.w;
         }
-        reinterpret_cast<float4 *>(p.o_part + (part0 + h) * D)[c] = a;
-        if (c == 0) {
-            p.m_part[part0 + h] = M;
-            p.l_part[part0 + h] = L;
+        if (whole) {
+            const float inv = L == 0.f ? 0.f : p.v_scale / L;
+            store_out(p, (qrow0 + h) * D + 4 * c, make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv));
+            if (p.lse && c == 0) p.lse[qrow0 + h] = lse_of(M, L);
+        } else {
+            reinterpret_cast<float4 *>(p.o_part + (part0 + h) * D)[c] = a;
+            if (c == 0) {
+                p.m_part[part0 + h] = M;
+                p.l_part[part0 + h] = L;
+            }
         }
+    }
+    // the CTA where a segment begins notes which CTAs hold its parts
+    if (unit0 == 0 && threadIdx.x == 0) {
+        // the last CTA whose range begins before the segment's end
+        const int64_t end = seg_end;
+        int last = (int)(((end - 1) * ctas) / total);
+        while (total * (last + 1) / ctas < end) ++last;
+        while (last > 0 && total * last / ctas >= end) --last;
+        p.seg_range[(size_t)b * per_seq + seg] = make_int2(blockIdx.x, last);
+    }
+    __syncthreads();       // O in shared memory is read before the next segment's copies
+    if (pos == seg_end && next_seq) { seq_at = seg_end; ++b; }
     }
 }
 
-// One CTA of dv / 4 threads per (sequence, head): the weight of each split, then its columns.
-template <class T>
-__global__ void __launch_bounds__(128) q4_merge_kernel(const DecodeParams p, int dv, T *__restrict__ out,
-                                                       float *__restrict__ lse) {
+// One CTA per (sequence, query head) merges the parts of a segment that several CTAs share: the
+// weights of up to CH parts at a time, then D / 4 columns x MERGE / (D / 4) parts in flight.  It also answers for
+// sequences without rows (o = 0, lse = -inf).
+constexpr int MERGE = 256;
+template <int D, int HPC>
+__global__ void __launch_bounds__(MERGE) q4_merge_split_kernel(const DecodeParams p) {
+    constexpr int COLS = D / 4, ROWS = MERGE / COLS;
+    __shared__ float4 red[ROWS][COLS];
+    __shared__ float wmax[MERGE / 32], wsum[MERGE / 32], w_of[MERGE];
+    const int b = blockIdx.y, head = blockIdx.x, G = p.Hq / p.heads, groups = (G + HPC - 1) / HPC;
+    const int kvh = head / G, gh = head - kvh * G, grp = gh / HPC, h = gh - grp * HPC;
+    const size_t row = (size_t)b * p.Hq + head;
+    const int col = threadIdx.x % COLS, r = threadIdx.x / COLS;
+    if (count_units(p, b) == 0) {
+        if (r == 0) store_out(p, row * D + 4 * col, make_float4(0.f, 0.f, 0.f, 0.f));
+        if (p.lse && threadIdx.x == 0) p.lse[row] = -INFINITY;
+        return;
+    }
+    const int2 range = p.seg_range[((size_t)b * p.heads + kvh) * groups + grp];
+    if (range.x == range.y) return;            // finished by its CTA
+    const int n = range.y - range.x + 1;
+    auto part = [&](int i) { return (2 * (size_t)(range.x + i) + (i == 0 ? 1 : 0)) * HPC + h; };
+    float M = -INFINITY;
+    for (int i = threadIdx.x; i < n; i += MERGE) M = fmaxf(M, p.m_part[part(i)]);
+    M = warp_max(M);
+    if ((threadIdx.x & 31) == 0) wmax[threadIdx.x >> 5] = M;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < MERGE / 32; ++w) M = fmaxf(M, wmax[w]);
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+    float L = 0.f;
+    for (int i0 = 0; i0 < n; i0 += MERGE) {
+        const int i = i0 + threadIdx.x;
+        float f = 0.f;
+        if (i < n) {
+            const float m = p.m_part[part(i)];
+            f = m == -INFINITY ? 0.f : exp2f(m - M);
+            L += f * p.l_part[part(i)];
+        }
+        w_of[threadIdx.x] = f;
+        __syncthreads();
+        const int here = min(MERGE, n - i0);
+#pragma unroll 4
+        for (int j = r; j < here; j += ROWS) {
+            const float wgt = w_of[j];
+            const float4 v = __ldcs(reinterpret_cast<const float4 *>(p.o_part + part(i0 + j) * D) + col);
+            a.x += wgt * v.x; a.y += wgt * v.y; a.z += wgt * v.z; a.w += wgt * v.w;
+        }
+        __syncthreads();
+    }
+    L = warp_sum(L);
+    if ((threadIdx.x & 31) == 0) wsum[threadIdx.x >> 5] = L;
+    red[r][col] = a;
+    __syncthreads();
+    L = 0.f;
+#pragma unroll
+    for (int w = 0; w < MERGE / 32; ++w) L += wsum[w];
+    if (r == 0) {
+#pragma unroll
+        for (int j = 1; j < ROWS; ++j) {
+            const float4 v = red[j][col];
+            a.x += v.x; a.y += v.y; a.z += v.z; a.w += v.w;
+        }
+        const float inv = L == 0.f ? 0.f : p.v_scale / L;
+        store_out(p, row * D + 4 * col, make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv));
+        if (p.lse && col == 0) p.lse[row] = lse_of(M, L);
+    }
+}
+
+// Latent rows: one CTA of dv / 4 threads per (sequence, head).  The loads of a group of splits are issued
+// before any arithmetic.
+__global__ void __launch_bounds__(128) q4_merge_kernel(const DecodeParams p, int dv) {
+    constexpr int GROUP = 10;
     const int h = blockIdx.x, b = blockIdx.y, c = threadIdx.x;
     const size_t row0 = (size_t)b * p.n_splits * p.Hq + h;
-    float M = -INFINITY;
-    for (int s = 0; s < p.n_splits; ++s) M = fmaxf(M, p.m_part[row0 + (size_t)s * p.Hq]);
-    float L = 0.f;
+    float M = -INFINITY, L = 0.f;
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int s = 0; s < p.n_splits; ++s) {
-        const size_t r = row0 + (size_t)s * p.Hq;
-        const float m = p.m_part[r], f = m == -INFINITY ? 0.f : exp2f(m - M);
-        const float4 v = __ldcs(reinterpret_cast<const float4 *>(p.o_part + r * dv) + c);
-        L += f * p.l_part[r];
-        a.x += f * v.x; a.y += f * v.y; a.z += f * v.z; a.w += f * v.w;
+    for (int s0 = 0; s0 < p.n_splits; s0 += GROUP) {
+        float4 v[GROUP];
+        float m[GROUP], l[GROUP];
+#pragma unroll
+        for (int j = 0; j < GROUP; ++j) {
+            m[j] = -INFINITY;
+            l[j] = 0.f;
+            v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (s0 + j < p.n_splits) {
+                const size_t r = row0 + (size_t)(s0 + j) * p.Hq;
+                v[j] = __ldcs(reinterpret_cast<const float4 *>(p.o_part + r * dv) + c);
+                m[j] = __ldg(p.m_part + r);
+                l[j] = __ldg(p.l_part + r);
+            }
+        }
+        float Mn = M;
+#pragma unroll
+        for (int j = 0; j < GROUP; ++j) Mn = fmaxf(Mn, m[j]);
+        const float r = M == -INFINITY ? 0.f : exp2f(M - Mn);
+        L *= r;
+        a.x *= r; a.y *= r; a.z *= r; a.w *= r;
+#pragma unroll
+        for (int j = 0; j < GROUP; ++j) {
+            const float f = m[j] == -INFINITY ? 0.f : exp2f(m[j] - Mn);
+            L += f * l[j];
+            a.x += f * v[j].x; a.y += f * v[j].y; a.z += f * v[j].z; a.w += f * v[j].w;
+        }
+        M = Mn;
     }
     // no rows at all: o = 0, lse = -inf.  A NaN sum (a NaN row in the set) stays NaN.
     const float inv = L == 0.f ? 0.f : p.v_scale / L;
-    Vec<T, 4> o;
-    o.v[0] = from_f32<T>(a.x * inv); o.v[1] = from_f32<T>(a.y * inv);
-    o.v[2] = from_f32<T>(a.z * inv); o.v[3] = from_f32<T>(a.w * inv);
-    *reinterpret_cast<Vec<T, 4> *>(out + ((size_t)b * p.Hq + h) * dv + 4 * c) = o;
-    if (lse && c == 0) lse[(size_t)b * p.Hq + h] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.69314718055994530942f;
-}
-
-int launch_merge(const DecodeParams &p, int B, int dv, int out_dtype, void *out, float *lse, cudaStream_t stream) {
-    const dim3 grid(p.Hq, B);
-    if (out_dtype == LSA_DTYPE_BF16)
-        q4_merge_kernel<<<grid, dv / 4, 0, stream>>>(p, dv, static_cast<__nv_bfloat16 *>(out), lse);
-    else if (out_dtype == LSA_DTYPE_F16)
-        q4_merge_kernel<<<grid, dv / 4, 0, stream>>>(p, dv, static_cast<__half *>(out), lse);
-    else
-        q4_merge_kernel<<<grid, dv / 4, 0, stream>>>(p, dv, static_cast<float *>(out), lse);
-    return check_launch("q4_merge_kernel");
+    store_out(p, ((size_t)b * p.Hq + h) * dv + 4 * c, make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv));
+    if (p.lse && c == 0) p.lse[(size_t)b * p.Hq + h] = lse_of(M, L);
 }
 
 static int max_units(int k, int max_window_len) { return (k + 63) / 64 + (max_window_len + 63) / 64 + 1; }
 
-// Splits of one (sequence, K/V head, head group): enough CTAs for two a multiprocessor, each
-// warp at least one unit.
-static int separate_splits(int B, int heads, int G, int units) {
+// CTAs of the separate K/V kernel: one wave (3 or 2 a multiprocessor), fewer where there would be less than a
+// unit for each warp even if every sequence had its longest row set.
+static int separate_ctas(int B, int heads, int G, int units) {
     const int hpc = G <= 8 ? 8 : 16, groups = (G + hpc - 1) / hpc;
-    const int64_t per = (int64_t)B * heads * groups;
-    const int64_t want = (2 * sm_count() + per - 1) / per;
-    return (int)lsa_max64(1, lsa_min64(want, (units + WARPS - 1) / WARPS));
+    const int64_t most = ((int64_t)B * heads * groups * (units + SETUP) + WARPS - 1) / WARPS;
+    return (int)lsa_max64(1, lsa_min64(sm_count() * (G <= 8 ? 3 : 2), most));
 }
 
 template <class C>
-static int launch_separate(const DecodeParams &p, int B, int G, cudaStream_t stream) {
-    const int groups = (G + C::HPC - 1) / C::HPC;
-    LSA_CUDA(cudaFuncSetAttribute(q4_decode_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM));
-    q4_decode_kernel<C><<<dim3(p.n_splits, p.heads * groups, B), WARPS * 32, C::SMEM, stream>>>(p);
-    return check_launch("q4_decode_kernel");
+static int launch_separate(const DecodeParams &p, int B, cudaStream_t stream) {
+    static std::atomic<uint64_t> done{0};
+    if (int rc = allow_shared(q4_decode_kernel<C>, C::SMEM, done)) return rc;
+    q4_decode_kernel<C><<<p.n_splits, WARPS * 32, C::SMEM, stream>>>(p, B);
+    if (int rc = check_launch("q4_decode_kernel")) return rc;
+    q4_merge_split_kernel<C::D, C::HPC><<<dim3(p.Hq, B), MERGE, 0, stream>>>(p);
+    return check_launch("q4_merge_split_kernel");
 }
 
 static bool supported(int Hq, int heads, int dqk, int dv, bool latent) {
@@ -481,7 +655,18 @@ static bool supported(int Hq, int heads, int dqk, int dv, bool latent) {
 
 static int splits_for(int B, int Hq, int heads, bool latent, int k, int max_window_len) {
     const int units = max_units(k, max_window_len);
-    return latent ? q4mla::splits(B, units) : separate_splits(B, heads, Hq / heads, units);
+    return latent ? q4mla::splits(B, units) : separate_ctas(B, heads, Hq / heads, units);
+}
+
+// Carves the workspace: partials of every split (latent), or two a CTA and the segments' ranges.
+static size_t carve(Carver &c, DecodeParams &p, int B, int dv, bool latent) {
+    const int G = p.Hq / p.heads, hpc = G <= 8 ? 8 : 16;
+    const size_t rows = latent ? (size_t)B * p.n_splits * p.Hq : (size_t)p.n_splits * 2 * hpc;
+    p.o_part = c.take<float>(rows * dv);
+    p.m_part = c.take<float>(rows);
+    p.l_part = c.take<float>(rows);
+    p.seg_range = c.take<int2>(latent ? 0 : (size_t)B * p.heads * ((G + hpc - 1) / hpc));
+    return align_up(c.used, 256);
 }
 
 }  // namespace q4
@@ -493,12 +678,11 @@ extern "C" size_t lsa_sparse_decode_q4_workspace_size(int B, int Hq, int heads, 
                                                       int max_window_len) {
     const bool latent = dqk != dv;
     if (!q4::supported(Hq, heads, dqk, dv, latent) || B < 1 || B > 65535 || k < 0 || max_window_len < 0) return 0;
-    const int ns = q4::splits_for(B, Hq, heads, latent, k, max_window_len);
+    q4::DecodeParams p = {};
+    p.Hq = Hq; p.heads = heads;
+    p.n_splits = q4::splits_for(B, Hq, heads, latent, k, max_window_len);
     Carver c(nullptr);
-    c.take<float>((size_t)B * ns * Hq * dv);
-    c.take<float>((size_t)B * ns * Hq);
-    c.take<float>((size_t)B * ns * Hq);
-    return align_up(c.used, 256);
+    return q4::carve(c, p, B, dv, latent);
 }
 
 extern "C" int lsa_sparse_decode_q4(int q_dtype, const void *q, const uint8_t *k_pool, float k_scale,
@@ -528,26 +712,27 @@ extern "C" int lsa_sparse_decode_q4(int q_dtype, const void *q, const uint8_t *k
                 "lsa_sparse_decode_q4: q, pools and out must be 16-byte aligned");
     LSA_REQUIRE(scale > 0.f && scale <= 1e30f && k_scale > 0.f && k_scale <= 1e30f && v_scale > 0.f && v_scale <= 1e30f,
                 LSA_ERR_INVALID_ARG, "lsa_sparse_decode_q4: scales must be positive and at most 1e30");
-    const size_t need = lsa_sparse_decode_q4_workspace_size(B, Hq, heads, dqk, dv, k, max_window_len);
-    LSA_REQUIRE(ws && ws_bytes >= need, LSA_ERR_WORKSPACE, "lsa_sparse_decode_q4: workspace of %zu bytes, %zu needed",
-                ws_bytes, need);
     q4::DecodeParams p = {};
+    p.Hq = Hq; p.heads = heads;
     p.n_splits = q4::splits_for(B, Hq, heads, latent, k, max_window_len);
     Carver c(ws);
-    p.o_part = c.take<float>((size_t)B * p.n_splits * Hq * dv);
-    p.m_part = c.take<float>((size_t)B * p.n_splits * Hq);
-    p.l_part = c.take<float>((size_t)B * p.n_splits * Hq);
+    const size_t need = q4::carve(c, p, B, dv, latent);
+    LSA_REQUIRE(ws && ws_bytes >= need, LSA_ERR_WORKSPACE, "lsa_sparse_decode_q4: workspace of %zu bytes, %zu needed",
+                ws_bytes, need);
     p.q = q; p.k_pool = k_pool; p.v_pool = v_pool; p.table = chunk_table; p.topk_idx = topk_idx;
     p.topk_count = topk_count; p.window_start = window_start; p.window_len = window_len; p.status = dev_status;
-    p.n_slots = n_slots; p.table_stride = table_stride; p.k = k; p.Hq = Hq; p.heads = heads;
+    p.n_slots = n_slots; p.table_stride = table_stride; p.k = k;
     p.scale_log2 = scale * k_scale * 1.4426950408889634f;
     p.v_scale = latent ? k_scale : v_scale;
     p.q_f16 = q_dtype == LSA_DTYPE_F16;
+    p.out = out; p.lse = lse; p.out_dtype = out_dtype;
     const int G = Hq / heads;
-    int rc;
-    if (latent) rc = q4mla::launch(p, B, stream);
-    else if (dqk == 128) rc = G <= 8 ? q4::launch_separate<q4::Cfg<128, 1>>(p, B, G, stream) : q4::launch_separate<q4::Cfg<128, 2>>(p, B, G, stream);
-    else rc = G <= 8 ? q4::launch_separate<q4::Cfg<64, 1>>(p, B, G, stream) : q4::launch_separate<q4::Cfg<64, 2>>(p, B, G, stream);
-    if (rc) return rc;
-    return q4::launch_merge(p, B, dv, out_dtype, out, lse, stream);
+    if (latent) {
+        if (int rc = q4mla::launch(p, B, stream)) return rc;
+        q4::q4_merge_kernel<<<dim3(Hq, B), dv / 4, 0, stream>>>(p, dv);
+        return check_launch("q4_merge_kernel");
+    }
+    if (dqk == 128)
+        return G <= 8 ? q4::launch_separate<q4::Cfg<128, 1>>(p, B, stream) : q4::launch_separate<q4::Cfg<128, 2>>(p, B, stream);
+    return G <= 8 ? q4::launch_separate<q4::Cfg<64, 1>>(p, B, stream) : q4::launch_separate<q4::Cfg<64, 2>>(p, B, stream);
 }

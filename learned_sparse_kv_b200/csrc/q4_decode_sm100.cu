@@ -594,7 +594,8 @@ int splits(int B, int max_units) {
 
 int launch(const DecodeParams &p, int B, cudaStream_t stream) {
     const size_t smem = sizeof(Smem) + 1024;
-    LSA_CUDA(cudaFuncSetAttribute(q4_mla_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
+    static std::atomic<uint64_t> done{0};
+    if (int rc = allow_shared(q4_mla_kernel, (int)smem, done)) return rc;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2 * p.n_splits, B, 1);
     cfg.blockDim = dim3(THREADS, 1, 1);

@@ -10,12 +10,17 @@ struct DecodeParams {
     const void *q;                  // [B, Hq, dqk] bf16 or f16
     const uint8_t *k_pool, *v_pool; // v_pool null: latent rows
     const int32_t *table, *topk_idx, *topk_count, *window_start, *window_len;
-    float *o_part, *m_part, *l_part;   // [B, splits, Hq, dv], [B, splits, Hq]
+    void *out;                      // [B, Hq, dv] of out_dtype
+    float *lse;                     // [B, Hq] or null
+    // Latent: [B, splits, Hq, dv] and [B, splits, Hq].  Separate: two parts a CTA, [CTAs, 2, heads of a CTA, dv],
+    // and the first and last CTA of every segment.
+    float *o_part, *m_part, *l_part;
+    int2 *seg_range;
     int32_t *status;
     int64_t n_slots;
-    int table_stride, k, Hq, heads, n_splits;
+    int table_stride, k, Hq, heads, n_splits;   // n_splits: CTA pairs a sequence (latent), CTAs in all (separate)
     float scale_log2, v_scale;      // scale_log2: scale * k_scale * log2(e)
-    int q_f16;
+    int q_f16, out_dtype;
 };
 
 // Units of one sequence: ceil(tk / 64) units of 64 top-k rows, then the window chunk by chunk
@@ -78,9 +83,6 @@ __device__ __forceinline__ float row_exponent(float amax, float &inv) {
     inv = __uint_as_float((254u - e) << 23);
     return __uint_as_float(e << 23);
 }
-
-// Writes out = sum_r 2^(m_r - M) O_r / sum and the natural-log LSE from the splits' partials.
-int launch_merge(const DecodeParams &p, int B, int dv, int out_dtype, void *out, float *lse, cudaStream_t stream);
 
 }  // namespace q4
 

@@ -435,35 +435,83 @@ def advance_window(window_start, window_len, by, new_len, *, stream=None):
 
 
 # ------------------------------------------- tables, norm + rotation ----
+#
+# These calls are short on the device, so the host side is kept short too: one check per tensor
+# (_arg), pointers as plain integers, no device switch unless the tensors are on another device.
 
 DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+_I32, _I64, _U8, _F32, _BF16 = torch.int32, torch.int64, torch.uint8, torch.float32, torch.bfloat16
 
 
 def _dtype(dt, name):
-    if dt not in DTYPES:
+    code = DTYPES.get(dt)
+    if code is None:
         raise LSAError(1, f"{name} must be bfloat16, float16 or float32, got {dt}")
-    return DTYPES[dt]
+    return code
 
 
-def _shape(t, shape, name):
+def _cuda(t, dims, name):
+    """Device index of a CUDA tensor of one of the given dimension counts."""
+    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dim() in dims):
+        raise LSAError(1, f"{name} must be a CUDA tensor of {' or '.join(map(str, dims))} dimensions")
+    return t.get_device()
+
+
+def _arg(t, dtype, shape, index, name):
+    """Address of a contiguous tensor of that type, shape and device."""
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == index \
+            and t.is_contiguous():
+        return t.data_ptr()
+    if not (isinstance(t, torch.Tensor) and t.is_cuda):
+        raise LSAError(1, f"{name} must be a CUDA tensor")
+    if t.dtype is not dtype:
+        raise LSAError(1, f"{name} must be {dtype}, got {t.dtype}")
     if tuple(t.shape) != tuple(shape):
         raise LSAError(1, f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.get_device() != index:
+        raise LSAError(1, f"{name} must be on cuda:{index}, like the first argument")
+    raise LSAError(1, f"{name} must be contiguous")
 
 
-def _same_device(dev, **tensors):
-    for name, t in tensors.items():
-        if t is not None and t.device != dev:
-            raise LSAError(1, f"{name} must be on {dev}, like the first argument")
+def _status(t, index):
+    if t is None:
+        return None
+    if t.dtype is _I32 and t.is_cuda and t.get_device() == index and t.numel() >= 1:
+        return t.data_ptr()
+    raise LSAError(1, f"status must be an int32 tensor on cuda:{index}")
 
 
-def _launch(dev, stream):
-    """The stream handle for a launch on `dev`, whatever the current device is."""
-    return _stream(stream if stream is not None else torch.cuda.current_stream(dev))
+class _NoSwitch:
+    def __enter__(self):
+        pass
+
+    def __exit__(self, *exc):
+        return False
 
 
-def _side(stream, dev, *fresh):
+_NO_SWITCH = _NoSwitch()
+
+
+def _on(index):
+    """Makes device `index` current for the call, if it is not."""
+    return _NO_SWITCH if torch.cuda.current_device() == index else torch.cuda.device(index)
+
+
+def _handle(index, stream):
+    return stream.cuda_stream if stream is not None else torch.cuda.current_stream(index).cuda_stream
+
+
+def _workspace(nbytes, ws, index):
+    if ws is None:
+        return torch.empty(nbytes if nbytes > 256 else 256, dtype=_U8, device=torch.device("cuda", index))
+    if not (ws.dtype is _U8 and ws.is_cuda and ws.get_device() == index and ws.is_contiguous()):
+        raise LSAError(1, f"ws must be a contiguous uint8 tensor on cuda:{index}")
+    return ws
+
+
+def _side(stream, index, *fresh):
     """Tensors made here on the current stream stay reserved until the work on `stream` is done."""
-    if stream is not None and stream != torch.cuda.current_stream(dev):
+    if stream is not None and stream != torch.cuda.current_stream(index):
         for t in fresh:
             t.record_stream(stream)
 
@@ -480,42 +528,57 @@ def build_tables(table, cached_len, new_len, n_slots, max_new, *, table_next=Non
     slot_map [max_new] int64, position [max_new] int32, new_offset [B + 1] int32, n_free [1] int32); map entries behind
     the last new token are -1.
     """
-    _dev(table, torch.int32, "table"); _dev(cached_len, torch.int32, "cached_len"); _dev(new_len, torch.int32, "new_len")
+    index = _cuda(table, (2,), "table")
     B, stride = table.shape
-    _shape(cached_len, (B,), "cached_len"); _shape(new_len, (B,), "new_len")
     dev = table.device
-    i32 = dict(dtype=torch.int32, device=dev)
-    with torch.cuda.device(dev):
-        table_next = torch.empty(B, stride, **i32) if table_next is None else _dev(table_next, torch.int32, "table_next")
-        slot_map = torch.empty(max_new, dtype=torch.int64, device=dev) if slot_map is None else \
-            _dev(slot_map, torch.int64, "slot_map")
-        position = torch.empty(max_new, **i32) if position is None else _dev(position, torch.int32, "position")
-        new_offset = torch.empty(B + 1, **i32) if new_offset is None else _dev(new_offset, torch.int32, "new_offset")
-        n_free = torch.empty(1, **i32) if n_free is None else _dev(n_free, torch.int32, "n_free")
-        _shape(table_next, (B, stride), "table_next"); _shape(slot_map, (max_new,), "slot_map")
-        _shape(position, (max_new,), "position"); _shape(new_offset, (B + 1,), "new_offset"); _shape(n_free, (1,), "n_free")
-        _same_device(dev, cached_len=cached_len, new_len=new_len, table_next=table_next, slot_map=slot_map,
-                     position=position, new_offset=new_offset, n_free=n_free, status=status, ws=ws)
-        ws = _ws(build_tables_workspace_size(B, stride, n_slots), dev, ws)
-        _check(_lib.lsa_build_tables(_ptr(table), stride, _ptr(cached_len), _ptr(new_len), B, n_slots, max_new,
-                                     _ptr(table_next), _ptr(slot_map), _ptr(position), _ptr(new_offset), _ptr(n_free),
-                                     _ptr(status), _ptr(ws), ws.numel(), _launch(dev, stream)))
-        _side(stream, dev, ws, table_next, slot_map, position, new_offset, n_free)
+    if max_new < 0:
+        raise LSAError(1, "max_new must not be negative")
+    with _on(index):
+        if table_next is None:
+            table_next = torch.empty_like(table)
+        if slot_map is None:
+            slot_map = torch.empty(max_new, dtype=_I64, device=dev)
+        if position is None:
+            position = torch.empty(max_new, dtype=_I32, device=dev)
+        if new_offset is None:
+            new_offset = torch.empty(B + 1, dtype=_I32, device=dev)
+        if n_free is None:
+            n_free = torch.empty(1, dtype=_I32, device=dev)
+        ws = _workspace(_lib.lsa_build_tables_workspace_size(B, stride, n_slots), ws, index)
+        _check(_lib.lsa_build_tables(
+            _arg(table, _I32, (B, stride), index, "table"), stride, _arg(cached_len, _I32, (B,), index, "cached_len"),
+            _arg(new_len, _I32, (B,), index, "new_len"), B, n_slots, max_new,
+            _arg(table_next, _I32, (B, stride), index, "table_next"), _arg(slot_map, _I64, (max_new,), index, "slot_map"),
+            _arg(position, _I32, (max_new,), index, "position"), _arg(new_offset, _I32, (B + 1,), index, "new_offset"),
+            _arg(n_free, _I32, (1,), index, "n_free"), _status(status, index), ws.data_ptr(), ws.numel(),
+            _handle(index, stream)))
+        if stream is not None:
+            _side(stream, index, ws, table_next, slot_map, position, new_offset, n_free)
     return table_next, slot_map, position, new_offset, n_free
 
 
-def _rows(t, name, dtype, T, D, heads=None):
-    """Checks [T, heads, D] rows with contiguous columns; returns (token stride, head stride)."""
-    if not (isinstance(t, torch.Tensor) and t.is_cuda):
-        raise LSAError(1, f"{name} must be a CUDA tensor")
-    if t.dtype != dtype:
-        raise LSAError(1, f"{name} must be {dtype}, got {t.dtype}")
-    if t.dim() != 3 or t.shape[0] != T or t.shape[2] != D or (heads is not None and t.shape[1] != heads):
-        raise LSAError(1, f"{name} must be [{T}, {'heads' if heads is None else heads}, {D}], got {tuple(t.shape)}")
-    if t.numel() and t.stride(2) != 1:
+def _rows(t, name, dtype, T, heads, D, index):
+    """Address, token stride and head stride of rows [T, heads, D] with contiguous columns."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == (T, heads, D) and t.get_device() == index):
+        if not (isinstance(t, torch.Tensor) and t.is_cuda):
+            raise LSAError(1, f"{name} must be a CUDA tensor")
+        if t.dtype is not dtype:
+            raise LSAError(1, f"{name} must be {dtype}, got {t.dtype}")
+        if t.get_device() != index:
+            raise LSAError(1, f"{name} must be on cuda:{index}, like the first argument")
+        raise LSAError(1, f"{name} must be [{T}, {heads}, {D}], got {tuple(t.shape)}")
+    st, sh, sc = t.stride()
+    if sc != 1 and D > 1 and T * heads > 0:
         raise LSAError(1, f"{name} must have contiguous columns")
     # the stride of a dimension of one row is never used; torch may report anything for it
-    return t.stride(0) if T > 1 else 0, t.stride(1) if t.shape[1] > 1 else 0
+    return t.data_ptr(), st if T > 1 else 0, sh if heads > 1 else 0
+
+
+def _norm(w, width, dtype, index, name):
+    if w is None:
+        return None, 0 if width is None else int(width)
+    n = w.numel() if width is None else int(width)
+    return (_arg(w, dtype, (n,), index, name) if n > 0 else None), n
 
 
 def qk_norm_rope(q, k, position, inv_freq, *, q_weight=None, k_weight=None, q_norm_width=None, k_norm_width=None,
@@ -527,40 +590,33 @@ def qk_norm_rope(q, k, position, inv_freq, *, q_weight=None, k_weight=None, q_no
     k_norm_width columns (default: the weight's length, or none without a weight); the rotation covers columns
     [rot_offset, rot_offset + rot_dim).  Returns (q_out, k_out); outputs may be the inputs.
     """
-    if not (isinstance(q, torch.Tensor) and q.is_cuda and q.dim() == 3):
-        raise LSAError(1, "q must be a CUDA tensor [T, heads, D]")
+    index = _cuda(q, (3,), "q")
     T, Hq, D = q.shape
-    dt, dev = q.dtype, q.device
+    dt = q.dtype
     code = _dtype(dt, "q")
-    _dev(position, torch.int32, "position"); _dev(inv_freq, torch.float32, "inv_freq")
-    _shape(position, (T,), "position")
-    if inv_freq.dim() != 1:
+    if not (isinstance(inv_freq, torch.Tensor) and inv_freq.dim() == 1):
         raise LSAError(1, "inv_freq must have one dimension")
-    widths = []
-    for name, w, n in (("q_weight", q_weight, q_norm_width), ("k_weight", k_weight, k_norm_width)):
-        if w is not None:
-            _dev(w, dt, name)
-        n = (0 if w is None else w.numel()) if n is None else int(n)
-        if w is not None and n > 0:
-            _shape(w, (n,), name)
-        widths.append(n)
-    with torch.cuda.device(dev):
-        q_out = torch.empty_like(q, memory_format=torch.contiguous_format) if q_out is None else q_out
-        if k is not None and k_out is None:
-            k_out = torch.empty_like(k, memory_format=torch.contiguous_format)
-        qs, qo = _rows(q, "q", dt, T, D), _rows(q_out, "q_out", dt, T, D, Hq)
-        ks, ko, Hk = (0, 0), (0, 0), 0
+    half = inv_freq.shape[0]
+    qw, qn = _norm(q_weight, q_norm_width, dt, index, "q_weight")
+    kw, kn = _norm(k_weight, k_norm_width, dt, index, "k_weight")
+    with _on(index):
+        if q_out is None:
+            q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
+        kp = ko = (None, 0, 0)
+        Hk = 0
         if k is not None:
-            ks = _rows(k, "k", dt, T, D)
+            _cuda(k, (3,), "k")
             Hk = k.shape[1]
-            ko = _rows(k_out, "k_out", dt, T, D, Hk)
-        _same_device(dev, k=k, position=position, inv_freq=inv_freq, q_weight=q_weight, k_weight=k_weight, q_out=q_out,
-                     k_out=k_out)
-        _check(_lib.lsa_qk_norm_rope(code, T, D, _ptr(q), *qs, Hq, _ptr(q_weight), widths[0], _ptr(q_out), *qo, _ptr(k),
-                                     *ks, Hk, _ptr(k_weight), widths[1], _ptr(k_out), *ko, float(eps), _ptr(position),
-                                     _ptr(inv_freq), int(rot_offset), 2 * inv_freq.numel(), int(bool(interleaved)),
-                                     _launch(dev, stream)))
-        _side(stream, dev, q_out, *([] if k_out is None else [k_out]))
+            if k_out is None:
+                k_out = torch.empty_like(k, memory_format=torch.contiguous_format)
+            kp, ko = _rows(k, "k", dt, T, Hk, D, index), _rows(k_out, "k_out", dt, T, Hk, D, index)
+        _check(_lib.lsa_qk_norm_rope(
+            code, T, D, *_rows(q, "q", dt, T, Hq, D, index), Hq, qw, qn, *_rows(q_out, "q_out", dt, T, Hq, D, index), *kp,
+            Hk, kw, kn, *ko, eps, _arg(position, _I32, (T,), index, "position"),
+            _arg(inv_freq, _F32, (half,), index, "inv_freq"), rot_offset, 2 * half, 1 if interleaved else 0,
+            _handle(index, stream)))
+        if stream is not None:
+            _side(stream, index, q_out, *([] if k is None else [k_out]))
     return q_out, k_out
 
 
@@ -579,96 +635,91 @@ def q4_pool(n_slots, heads, width, device="cuda"):
     return torch.zeros(n_slots, heads, q4_chunk_bytes(width), dtype=torch.uint8, device=device)
 
 
-def _pool(t, name, heads=None, width=None, n_slots=None):
-    _dev(t, torch.uint8, name)
-    if t.dim() != 3 or t.shape[2] % 576 or t.shape[2] == 0:
-        raise LSAError(1, f"{name} must be a 4-bit pool [n_slots, heads, 36 * width], got {tuple(t.shape)}")
-    for what, n, dim in (("slots", n_slots, 0), ("heads", heads, 1)):
-        if n is not None and t.shape[dim] != n:
-            raise LSAError(1, f"{name} must have {n} {what}, got {t.shape[dim]}")
-    if width is not None and t.shape[2] != 36 * width:
-        raise LSAError(1, f"{name} must hold rows of {width} values, got {t.shape[2] // 36}")
-    return t
+def _pool_shape(t, name):
+    """(slots, heads, width) of a 4-bit pool."""
+    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dim() == 3 and t.shape[2] % 576 == 0 and t.shape[2] > 0):
+        raise LSAError(1, f"{name} must be a 4-bit pool on a CUDA device, [n_slots, heads, 36 * width] uint8")
+    n, heads, nb = t.shape
+    return n, heads, nb // 36
 
 
 def _q4_rows(x, name):
     """[T, width] rows are one head."""
-    if not (isinstance(x, torch.Tensor) and x.is_cuda and x.dim() in (2, 3)):
-        raise LSAError(1, f"{name} must be a CUDA tensor [T, heads, width] or [T, width]")
-    return x.unsqueeze(1) if x.dim() == 2 else x
+    if _cuda(x, (2, 3), name) >= 0 and x.dim() == 2:
+        return x.unsqueeze(1)
+    return x
 
 
 def write_q4(k, k_pool, slot_map, *, v=None, v_pool=None, k_scale=1.0, v_scale=1.0, status=None, stream=None):
     """Quantises rows k [T, heads, width] (and v) into 4-bit pools at slot_map [T] int64 (slot * 64 + row, -1: skip)."""
     k = _q4_rows(k, "k")
+    index, dt = k.get_device(), k.dtype
     T, heads, kw = k.shape
-    dt, dev = k.dtype, k.device
     code = _dtype(dt, "k")
-    _dev(slot_map, torch.int64, "slot_map"); _shape(slot_map, (T,), "slot_map")
-    _pool(k_pool, "k_pool", heads, kw)
-    ks, vs, vw = _rows(k, "k", dt, T, kw), (0, 0), 0
+    n_slots = _pool_shape(k_pool, "k_pool")[0]
     if (v is None) != (v_pool is None):
         raise LSAError(1, "v and v_pool come together")
+    vp, vw, vpool = (None, 0, 0), 0, None
     if v is not None:
         v = _q4_rows(v, "v")
         vw = v.shape[2]
-        vs = _rows(v, "v", dt, T, vw, heads)
-        _pool(v_pool, "v_pool", heads, vw, k_pool.shape[0])
-    _same_device(dev, k_pool=k_pool, slot_map=slot_map, v=v, v_pool=v_pool, status=status)
-    with torch.cuda.device(dev):
-        _check(_lib.lsa_write_q4(code, T, heads, _ptr(k), *ks, kw, _ptr(k_pool), float(k_scale), _ptr(v), *vs, vw,
-                                 _ptr(v_pool), float(v_scale), k_pool.shape[0], _ptr(slot_map), _ptr(status),
-                                 _launch(dev, stream)))
+        vp = _rows(v, "v", dt, T, heads, vw, index)
+        vpool = _arg(v_pool, _U8, (n_slots, heads, 36 * vw), index, "v_pool")
+    with _on(index):
+        _check(_lib.lsa_write_q4(
+            code, T, heads, *_rows(k, "k", dt, T, heads, kw, index), kw,
+            _arg(k_pool, _U8, (n_slots, heads, 36 * kw), index, "k_pool"), k_scale, *vp, vw, vpool, v_scale, n_slots,
+            _arg(slot_map, _I64, (T,), index, "slot_map"), _status(status, index), _handle(index, stream)))
 
 
 def append_token_q4(new_k, new_v, new_li, k_pool, v_pool, li_pool, chunk_table, window_start, window_len, *,
                     k_scale=1.0, v_scale=1.0, status=None, stream=None):
     """append_token for 4-bit pools: new_k [B, heads, width] (or [B, width]), new_v likewise or None (latent)."""
     new_k = _q4_rows(new_k, "new_k")
+    index, dt = new_k.get_device(), new_k.dtype
     B, heads, kw = new_k.shape
-    dt, dev = new_k.dtype, new_k.device
     code = _dtype(dt, "new_k")
-    _dev(new_k, dt, "new_k"); _pool(k_pool, "k_pool", heads, kw)
-    vw, dl = 0, 0
+    n_slots = _pool_shape(k_pool, "k_pool")[0]
     if (new_v is None) != (v_pool is None):
         raise LSAError(1, "new_v and v_pool come together")
+    vw = dl = 0
+    vp = vpool = li = lip = None
     if new_v is not None:
-        new_v = _dev(_q4_rows(new_v, "new_v"), dt, "new_v")
+        new_v = _q4_rows(new_v, "new_v")
         vw = new_v.shape[2]
-        _shape(new_v, (B, heads, vw), "new_v"); _pool(v_pool, "v_pool", heads, vw, k_pool.shape[0])
+        vp = _arg(new_v, dt, (B, heads, vw), index, "new_v")
+        vpool = _arg(v_pool, _U8, (n_slots, heads, 36 * vw), index, "v_pool")
     if new_li is not None or li_pool is not None:
-        _dev(new_li, torch.bfloat16, "new_li"); _dev(li_pool, torch.bfloat16, "li_pool")
-        dl = li_pool.shape[-1]
-        _shape(new_li, (B, dl), "new_li"); _shape(li_pool, (k_pool.shape[0], CHUNK, dl), "li_pool")
-    for name, t in (("chunk_table", chunk_table), ("window_start", window_start), ("window_len", window_len)):
-        _dev(t, torch.int32, name)
-    stride = chunk_table.shape[-1]
-    _shape(chunk_table, (B, stride), "chunk_table"); _shape(window_start, (B,), "window_start")
-    _shape(window_len, (B,), "window_len")
-    _same_device(dev, new_v=new_v, new_li=new_li, k_pool=k_pool, v_pool=v_pool, li_pool=li_pool,
-                 chunk_table=chunk_table, window_start=window_start, window_len=window_len, status=status)
-    with torch.cuda.device(dev):
-        _check(_lib.lsa_append_token_q4(code, heads, _ptr(new_k), kw, _ptr(k_pool), float(k_scale), _ptr(new_v), vw,
-                                        _ptr(v_pool), float(v_scale), _ptr(new_li), _ptr(li_pool), dl, k_pool.shape[0],
-                                        _ptr(chunk_table), stride, _ptr(window_start), _ptr(window_len), B,
-                                        _ptr(status), _launch(dev, stream)))
+        _cuda(li_pool, (3,), "li_pool")
+        dl = li_pool.shape[2]
+        li, lip = _arg(new_li, _BF16, (B, dl), index, "new_li"), _arg(li_pool, _BF16, (n_slots, CHUNK, dl), index, "li_pool")
+    _cuda(chunk_table, (2,), "chunk_table")
+    stride = chunk_table.shape[1]
+    with _on(index):
+        _check(_lib.lsa_append_token_q4(
+            code, heads, _arg(new_k, dt, (B, heads, kw), index, "new_k"), kw,
+            _arg(k_pool, _U8, (n_slots, heads, 36 * kw), index, "k_pool"), k_scale, vp, vw, vpool, v_scale, li, lip, dl,
+            n_slots, _arg(chunk_table, _I32, (B, stride), index, "chunk_table"), stride,
+            _arg(window_start, _I32, (B,), index, "window_start"), _arg(window_len, _I32, (B,), index, "window_len"), B,
+            _status(status, index), _handle(index, stream)))
 
 
 def read_q4(pool, slot_map, *, scale=1.0, out=None, out_dtype=torch.bfloat16, status=None, stream=None):
     """Rows slot_map [T] of a 4-bit pool as values [T, heads, width] (zeros where slot_map is -1)."""
-    _pool(pool, "pool"); _dev(slot_map, torch.int64, "slot_map")
-    n_slots, heads, nb = pool.shape
-    dev, T = pool.device, slot_map.numel()
-    _shape(slot_map, (T,), "slot_map")
-    with torch.cuda.device(dev):
+    n_slots, heads, width = _pool_shape(pool, "pool")
+    index = pool.get_device()
+    _cuda(slot_map, (1,), "slot_map")
+    T = slot_map.shape[0]
+    with _on(index):
         if out is None:
-            out = torch.empty(T, heads, nb // 36, dtype=out_dtype, device=dev)
-        code = _dtype(out.dtype, "out")
-        _dev(out, out.dtype, "out"); _shape(out, (T, heads, nb // 36), "out")
-        _same_device(dev, slot_map=slot_map, out=out, status=status)
-        _check(_lib.lsa_read_q4(_ptr(pool), n_slots, heads, nb // 36, float(scale), _ptr(slot_map), T, code, _ptr(out),
-                                _ptr(status), _launch(dev, stream)))
-        _side(stream, dev, out)
+            _dtype(out_dtype, "out")
+            out = torch.empty(T, heads, width, dtype=out_dtype, device=pool.device)
+        _check(_lib.lsa_read_q4(
+            _arg(pool, _U8, (n_slots, heads, 36 * width), index, "pool"), n_slots, heads, width, scale,
+            _arg(slot_map, _I64, (T,), index, "slot_map"), T, _dtype(out.dtype, "out"),
+            _arg(out, out.dtype, (T, heads, width), index, "out"), _status(status, index), _handle(index, stream)))
+        if stream is not None:
+            _side(stream, index, out)
     return out
 
 
@@ -684,44 +735,37 @@ def sparse_decode_q4(q, k_pool, v_pool, chunk_table, topk_idx, topk_count, windo
 
     Returns (out [B, Hq, dv] of out_dtype, lse [B, Hq] fp32 or None).
     """
-    if not (isinstance(q, torch.Tensor) and q.is_cuda and q.dim() == 3):
-        raise LSAError(1, "q must be a CUDA tensor [B, Hq, dqk]")
+    index = _cuda(q, (3,), "q")
     B, Hq, dqk = q.shape
     dev = q.device
-    q_code = _dtype(q.dtype, "q")
-    _dev(q, q.dtype, "q"); _pool(k_pool, "k_pool", width=dqk)
-    n_slots, heads, _ = k_pool.shape
-    if v_pool is not None:
-        _pool(v_pool, "v_pool", heads, dv, n_slots)
-    k = 0
+    n_slots, heads, _ = _pool_shape(k_pool, "k_pool")
+    vpool = None if v_pool is None else _arg(v_pool, _U8, (n_slots, heads, 36 * dv), index, "v_pool")
+    k, ti, tc = 0, None, None
     if topk_idx is not None:
-        _dev(topk_idx, torch.int32, "topk_idx"); _dev(topk_count, torch.int32, "topk_count")
-        k = topk_idx.shape[-1]
-        _shape(topk_idx, (B, k), "topk_idx"); _shape(topk_count, (B,), "topk_count")
-    for name, t in (("chunk_table", chunk_table), ("window_start", window_start), ("window_len", window_len)):
-        _dev(t, torch.int32, name)
-    stride = chunk_table.shape[-1]
-    _shape(chunk_table, (B, stride), "chunk_table"); _shape(window_start, (B,), "window_start")
-    _shape(window_len, (B,), "window_len")
-    with torch.cuda.device(dev):
+        _cuda(topk_idx, (2,), "topk_idx")
+        k = topk_idx.shape[1]
+        if k:
+            ti, tc = _arg(topk_idx, _I32, (B, k), index, "topk_idx"), _arg(topk_count, _I32, (B,), index, "topk_count")
+    _cuda(chunk_table, (2,), "chunk_table")
+    stride = chunk_table.shape[1]
+    with _on(index):
         if out is None:
+            _dtype(out_dtype, "out")
             out = torch.empty(B, Hq, dv, dtype=out_dtype, device=dev)
-        o_code = _dtype(out.dtype, "out")
-        _dev(out, out.dtype, "out"); _shape(out, (B, Hq, dv), "out")
         if lse is None and want_lse:
-            lse = torch.empty(B, Hq, dtype=torch.float32, device=dev)
-        if lse is not None:
-            _dev(lse, torch.float32, "lse"); _shape(lse, (B, Hq), "lse")
-        _same_device(dev, k_pool=k_pool, v_pool=v_pool, chunk_table=chunk_table, topk_idx=topk_idx,
-                     topk_count=topk_count, window_start=window_start, window_len=window_len, out=out, lse=lse,
-                     status=status, ws=ws)
-        ws = _ws(sparse_decode_q4_workspace_size(B, Hq, heads, dqk, dv, k, max_window_len), dev, ws)
-        _check(_lib.lsa_sparse_decode_q4(q_code, _ptr(q), _ptr(k_pool), float(k_scale), _ptr(v_pool), float(v_scale),
-                                         n_slots, heads, _ptr(chunk_table), stride, _ptr(topk_idx if k else None),
-                                         _ptr(topk_count if k else None), k, _ptr(window_start), _ptr(window_len),
-                                         max_window_len, B, Hq, dqk, dv, float(scale), o_code, _ptr(out), _ptr(lse),
-                                         _ptr(status), _ptr(ws), ws.numel(), _launch(dev, stream)))
-        _side(stream, dev, ws, out, *([] if lse is None else [lse]))
+            lse = torch.empty(B, Hq, dtype=_F32, device=dev)
+        ws = _workspace(_lib.lsa_sparse_decode_q4_workspace_size(B, Hq, heads, dqk, dv, k, max_window_len), ws, index)
+        _check(_lib.lsa_sparse_decode_q4(
+            _dtype(q.dtype, "q"), _arg(q, q.dtype, (B, Hq, dqk), index, "q"),
+            _arg(k_pool, _U8, (n_slots, heads, 36 * dqk), index, "k_pool"), k_scale, vpool, v_scale, n_slots, heads,
+            _arg(chunk_table, _I32, (B, stride), index, "chunk_table"), stride, ti, tc, k,
+            _arg(window_start, _I32, (B,), index, "window_start"), _arg(window_len, _I32, (B,), index, "window_len"),
+            max_window_len, B, Hq, dqk, dv, scale, _dtype(out.dtype, "out"),
+            _arg(out, out.dtype, (B, Hq, dv), index, "out"),
+            None if lse is None else _arg(lse, _F32, (B, Hq), index, "lse"), _status(status, index), ws.data_ptr(),
+            ws.numel(), _handle(index, stream)))
+        if stream is not None:
+            _side(stream, index, ws, out, *([] if lse is None else [lse]))
     return out, lse
 
 

@@ -294,6 +294,11 @@ def test_attention_skips_and_flags_bad_pages(L, latent):
     c["start"][0] = -64                         # no window at all
     out, lse = _run(L, c, st=st)
     _check(c, out, lse)
+    c["start"][:], c["count"][:] = -64, 0       # nothing anywhere
+    st.zero_()
+    out, lse = _run(L, c, st=st)
+    assert st.item() == L.DEV_INDEX
+    _check(c, out, lse)
 
 
 @pytest.mark.parametrize("latent", [False, True])
