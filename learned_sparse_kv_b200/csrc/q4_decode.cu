@@ -13,8 +13,9 @@
 //    head, and the dequantised codes are the A operand straight from registers.
 //  - The contraction index of a product may be permuted freely.  For S^T lane t of a row's four
 //    lanes takes columns D/4 t .. D/4 t + D/4 - 1, contiguous codes: one 16-byte shared load; for
-//    O^T lane group g takes value columns D/8 g .. , contiguous again, and the tokens pair up by
-//    byte permutes of two tokens' f16 pairs.
+//    O^T lane group g takes value columns D/8 g .. , contiguous again.  There a register holds two
+//    tokens of one column: the nibbles of two tokens' words are interleaved before the conversion (four
+//    operations for 16 values), and their scales are a pair likewise.
 //  - P^T goes from the accumulator layout to the operand layout with movmatrix, no memory.
 // The grid is one wave of CTAs.  All units of all (sequence, K/V head, group of query heads) segments are
 // counted on the device and dealt to the CTAs in equal contiguous ranges, so ragged lengths cost
@@ -55,6 +56,15 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Bits of a where the mask is set, of b elsewhere.
+__device__ __forceinline__ uint32_t select_bits(uint32_t mask, uint32_t a, uint32_t b) { return (a & mask) | (b & ~mask); }
 
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
     uint32_t d;
@@ -281,7 +291,7 @@ __global__ void __launch_bounds__(WARPS * 32, C::CTAS) q4_decode_kernel(const De
         amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
         amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
         float inv;
-        const float e = row_exponent(amax, inv) * p.scale_log2;
+        const float e = fmaxf(row_exponent(amax, inv) * p.scale_log2, 1.2e-38f);   // not 0: 0 * -inf is NaN
         smul[n][0] = __shfl_sync(0xffffffffu, e, 8 * t);        // head 2t: lane (2t, 0)
         smul[n][1] = __shfl_sync(0xffffffffu, e, 8 * t + 4);
 #pragma unroll
@@ -314,6 +324,19 @@ __global__ void __launch_bounds__(WARPS * 32, C::CTAS) q4_decode_kernel(const De
             continue;
         }
         const uint32_t ks = ring + (i % C::STAGES) * C::STAGE, vs = ks + C::HALF;
+        const bool full = (lo & hi) == 0xffffffffu;
+        if (!full) {
+            // rows outside the set may hold anything, NaN scales too: their V scales become 0 (and their scores,
+            // below, -inf)
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+                if (!((n ? hi : lo) >> lane & 1u)) {
+                    const uint32_t at = vs + 64 * C::CODE + (lane + 32 * n) * C::SCALES;
+                    asm volatile("st.shared.u32 [%0], %1;" ::"r"(at), "r"(0) : "memory");
+                    if constexpr (D == 128) asm volatile("st.shared.u32 [%0], %1;" ::"r"(at + 4), "r"(0) : "memory");
+                }
+            __syncwarp();
+        }
 
         // ---- S^T = K Q^T: four tiles of 16 rows
         float s[4][NH][4];
@@ -361,18 +384,23 @@ __global__ void __launch_bounds__(WARPS * 32, C::CTAS) q4_decode_kernel(const De
         uint32_t pt[4][NH][2];
 #pragma unroll
         for (int n = 0; n < NH; ++n) {
+            if (!full) {
+#pragma unroll
+                for (int mt = 0; mt < 4; ++mt) {
+                    const uint32_t half = mt < 2 ? lo : hi;
+                    if (!((half >> (16 * (mt & 1) + g)) & 1u)) s[mt][n][0] = s[mt][n][1] = -INFINITY;
+                    if (!((half >> (16 * (mt & 1) + g + 8)) & 1u)) s[mt][n][2] = s[mt][n][3] = -INFINITY;
+                }
+            }
+            // the factor is positive: the maximum of the raw products is the scores'
             float mx0 = -INFINITY, mx1 = -INFINITY;
 #pragma unroll
             for (int mt = 0; mt < 4; ++mt) {
-                const uint32_t half = mt < 2 ? lo : hi;
-                const bool v0 = (half >> (16 * (mt & 1) + g)) & 1u, v1 = (half >> (16 * (mt & 1) + g + 8)) & 1u;
-                s[mt][n][0] = v0 ? s[mt][n][0] * smul[n][0] : -INFINITY;
-                s[mt][n][1] = v0 ? s[mt][n][1] * smul[n][1] : -INFINITY;
-                s[mt][n][2] = v1 ? s[mt][n][2] * smul[n][0] : -INFINITY;
-                s[mt][n][3] = v1 ? s[mt][n][3] * smul[n][1] : -INFINITY;
                 mx0 = fmaxf(mx0, fmaxf(s[mt][n][0], s[mt][n][2]));
                 mx1 = fmaxf(mx1, fmaxf(s[mt][n][1], s[mt][n][3]));
             }
+            mx0 *= smul[n][0];
+            mx1 *= smul[n][1];
 #pragma unroll
             for (int q = 4; q < 32; q *= 2) {
                 mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, q));
@@ -380,7 +408,7 @@ __global__ void __launch_bounds__(WARPS * 32, C::CTAS) q4_decode_kernel(const De
             }
             const bool move0 = mx0 > m_ref[n][0] + RESCALE, move1 = mx1 > m_ref[n][1] + RESCALE;
             if (__any_sync(0xffffffffu, move0 || move1)) {
-                const float a0 = move0 ? exp2f(m_ref[n][0] - mx0) : 1.f, a1 = move1 ? exp2f(m_ref[n][1] - mx1) : 1.f;
+                const float a0 = move0 ? ex2(m_ref[n][0] - mx0) : 1.f, a1 = move1 ? ex2(m_ref[n][1] - mx1) : 1.f;
                 if (move0) m_ref[n][0] = mx0;
                 if (move1) m_ref[n][1] = mx1;
                 l[n][0] *= a0;
@@ -395,8 +423,8 @@ __global__ void __launch_bounds__(WARPS * 32, C::CTAS) q4_decode_kernel(const De
             const float r1 = m_ref[n][1] == -INFINITY ? 0.f : m_ref[n][1] - P_SHIFT;
 #pragma unroll
             for (int mt = 0; mt < 4; ++mt) {
-                const float p0 = exp2f(s[mt][n][0] - r0), p1 = exp2f(s[mt][n][1] - r1);
-                const float p2 = exp2f(s[mt][n][2] - r0), p3 = exp2f(s[mt][n][3] - r1);
+                const float p0 = ex2(fmaf(s[mt][n][0], smul[n][0], -r0)), p1 = ex2(fmaf(s[mt][n][1], smul[n][1], -r1));
+                const float p2 = ex2(fmaf(s[mt][n][2], smul[n][0], -r0)), p3 = ex2(fmaf(s[mt][n][3], smul[n][1], -r1));
                 l[n][0] += p0 + p2;
                 l[n][1] += p1 + p3;
                 pt[mt][n][0] = transpose8x8(pack_f16x2(p0, p1));
@@ -407,9 +435,8 @@ __global__ void __launch_bounds__(WARPS * 32, C::CTAS) q4_decode_kernel(const De
         // ---- O^T += V^T P^T: four blocks of 16 rows as the contraction
 #pragma unroll
         for (int mt = 0; mt < 4; ++mt) {
-            const uint32_t half = mt < 2 ? lo : hi;
             // the lane's four rows: 2t, 2t + 1, 2t + 8, 2t + 9 of the block
-            uint32_t code[4][D / 64], sc[4];
+            uint32_t code[4][D / 64], byte[4];
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 const int in = 2 * t + (q & 1) + 8 * (q >> 1), r = 16 * mt + in, vr = v_row(r);
@@ -420,25 +447,22 @@ __global__ void __launch_bounds__(WARPS * 32, C::CTAS) q4_decode_kernel(const De
                 } else {
                     code[q][0] = ld_shared<uint32_t>(vs + vr * 32 + g * 4);
                 }
-                // a row outside the set may hold anything, a NaN scale too: its scale becomes 0
-                const uint32_t sb = ld_shared_u8(vs + 64 * C::CODE + r * C::SCALES + (D == 128 ? g : g >> 1));
-                const bool there = (half >> (16 * (mt & 1) + in)) & 1u;
-                sc[q] = dup_lo(e4m3x2_to_f16(there ? sb : 0u));
+                byte[q] = ld_shared_u8(vs + 64 * C::CODE + r * C::SCALES + (D == 128 ? g : g >> 1));
             }
+            const uint32_t s01 = e4m3x2_to_f16(byte[0] | byte[1] << 8), s23 = e4m3x2_to_f16(byte[2] | byte[3] << 8);
 #pragma unroll
             for (int w = 0; w < D / 64; ++w) {
-                uint32_t v[4][4];
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    e2m1x8_to_f16(code[q][w], v[q]);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) v[q][j] = hmul2(v[q][j], sc[q]);
-                }
+                // even and odd columns of the word, two rows a byte
+                uint32_t e01[4], o01[4], e23[4], o23[4];
+                e2m1x8_to_f16(select_bits(0x0f0f0f0fu, code[0][w], code[1][w] << 4), e01);
+                e2m1x8_to_f16(select_bits(0x0f0f0f0fu, code[0][w] >> 4, code[1][w]), o01);
+                e2m1x8_to_f16(select_bits(0x0f0f0f0fu, code[2][w], code[3][w] << 4), e23);
+                e2m1x8_to_f16(select_bits(0x0f0f0f0fu, code[2][w] >> 4, code[3][w]), o23);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    // columns 2 (4w + j) and + 1 of the lane group's D / 8, tokens paired
-                    const uint32_t a0 = __byte_perm(v[0][j], v[1][j], 0x5410), a1 = __byte_perm(v[0][j], v[1][j], 0x7632);
-                    const uint32_t a2 = __byte_perm(v[2][j], v[3][j], 0x5410), a3 = __byte_perm(v[2][j], v[3][j], 0x7632);
+                    // columns 2 (4w + j) and + 1 of the lane group's D / 8
+                    const uint32_t a0 = hmul2(e01[j], s01), a1 = hmul2(o01[j], s01);
+                    const uint32_t a2 = hmul2(e23[j], s23), a3 = hmul2(o23[j], s23);
 #pragma unroll
                     for (int n = 0; n < NH; ++n) mma_f16(o[4 * w + j][n], a0, a1, a2, a3, pt[mt][n][0], pt[mt][n][1]);
                 }
