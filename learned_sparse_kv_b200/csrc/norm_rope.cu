@@ -9,17 +9,25 @@
 //
 // A row is read once into registers, by a group of LPR lanes.  A lane takes "items": both
 // vectors of a rotated pair (so the partner is always its own), or one vector outside the
-// rotation; an interleaved pair lies inside one vector.  The angle is taken in 64 bits: at
-// position 5e5 the product has 20 bits before the point, and fp32 would leave it an error of
-// 0.03 rad; turns = position * inv_freq / 2 pi, minus its nearest integer, then sincospi in fp32.
-// A CTA computes its tokens' cosines and sines once, into shared memory.
+// rotation; an interleaved pair lies inside one vector.  A group keeps to one token and walks its
+// heads; the next head's vectors are loaded while this one's are worked on.
+// Norm weight, cosine and sine are folded once per token into two coefficients a value: with
+// n = x / rms,  out = n P + n_partner Q,  P = w cos, Q = -+ w_partner sin (w and 0 outside the rotation).
+// That leaves about 150 instructions for the 16 values a lane has of a row; with weights converted
+// and three products a value for every head it was 520, and the issue slots were the bound (65 us for
+// 8192 tokens of 40 rows of 128, now 36.5; several heads in flight at fewer warps: 110 us).
+// The angle is taken in 64 bits: at position 5e5 the product has 20 bits before the point, and
+// fp32 would leave it an error of 0.03 rad; turns = position * inv_freq / 2 pi, minus its nearest
+// integer, then sincospi in fp32.  A CTA computes its tokens' cosines and sines once, into shared
+// memory, laid out so that neighbouring lanes read neighbouring words.
+// Bound by memory: 4 bytes a bf16 value.
 #include "nvtx_range.cuh"
 #include "q4.cuh"
 
 namespace lsa {
 namespace rope {
 
-constexpr int THREADS = 256;
+constexpr int THREADS = 128;
 constexpr int MAX_ANGLES = 1024;   // (cos, sin) pairs a CTA holds: tokens x rot / 2
 
 struct Side {
@@ -28,6 +36,7 @@ struct Side {
     const void *w;
     int64_t token_stride, head_stride, out_token_stride, out_head_stride;
     int heads, norm_width;
+    float inv_width;  // 1 / norm_width
 };
 
 struct Params {
@@ -37,11 +46,10 @@ struct Params {
     int64_t T;
     int D, ro, rd;
     int tokens;       // tokens a CTA takes
-    int row_blocks;   // CTAs that share those tokens' rows (grid.y)
+    int per_token;    // lane groups of a CTA that share a token's heads: tokens * per_token = THREADS / LPR
     float eps;
 };
 
-// V: elements of a vector; LPR: lanes of a row; ITEMS: items of a lane.
 // SCALAR: rows whose addresses allow no vector access are moved element by element.
 template <class T, int V, bool SCALAR>
 __device__ __forceinline__ Vec<T, V> load_vec(const T *src) {
@@ -61,113 +69,205 @@ __device__ __forceinline__ void store_vec(T *dst, const Vec<T, V> &v) {
     }
 }
 
+// Pairs of elements: two from a 32-bit word (16-bit types), and back, rounding to nearest even.
+template <class T> struct Two;
+template <> struct Two<__nv_bfloat16> {
+    static __device__ __forceinline__ float2 get(const Vec<__nv_bfloat16, 2> &v) {
+        const uint32_t w = *reinterpret_cast<const uint32_t *>(&v);
+        return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+    }
+    static __device__ __forceinline__ void put(Vec<__nv_bfloat16, 2> &v, float a, float b) {
+        *reinterpret_cast<uint32_t *>(&v) = pack_bf16x2(a, b);
+    }
+};
+template <> struct Two<__half> {
+    static __device__ __forceinline__ float2 get(const Vec<__half, 2> &v) {
+        return __half22float2(*reinterpret_cast<const __half2 *>(&v));
+    }
+    static __device__ __forceinline__ void put(Vec<__half, 2> &v, float a, float b) {
+        *reinterpret_cast<uint32_t *>(&v) = q4::pack_f16x2(a, b);
+    }
+};
+template <> struct Two<float> {
+    static __device__ __forceinline__ float2 get(const Vec<float, 2> &v) { return make_float2(v.v[0], v.v[1]); }
+    static __device__ __forceinline__ void put(Vec<float, 2> &v, float a, float b) { v.v[0] = a; v.v[1] = b; }
+};
+template <class T, int V>
+__device__ __forceinline__ void widen(const Vec<T, V> &v, float (&x)[V]) {
+    if constexpr (V == 1) {
+        x[0] = to_f32(v.v[0]);
+    } else {
+#pragma unroll
+        for (int j = 0; j < V; j += 2) {
+            const float2 f = Two<T>::get(*reinterpret_cast<const Vec<T, 2> *>(&v.v[j]));
+            x[j] = f.x;
+            x[j + 1] = f.y;
+        }
+    }
+}
+template <class T, int V>
+__device__ __forceinline__ Vec<T, V> narrow(const float (&x)[V]) {
+    Vec<T, V> v;
+    if constexpr (V == 1) {
+        v.v[0] = from_f32<T>(x[0]);
+    } else {
+#pragma unroll
+        for (int j = 0; j < V; j += 2) Two<T>::put(*reinterpret_cast<Vec<T, 2> *>(&v.v[j]), x[j], x[j + 1]);
+    }
+    return v;
+}
+
+// V: elements of a vector; LPR: lanes of a row; ITEMS: items of a lane.  V > 2 divides every bound of the row
+// (rotation, norm widths); V <= 2 moves and checks element by element.
 template <class T, int V, int LPR, int ITEMS, bool INTER>
-__global__ void __launch_bounds__(THREADS) norm_rope_kernel(const Params p) {
+__global__ void __launch_bounds__(THREADS, ITEMS == 1 ? 5 : 1) norm_rope_kernel(const Params p) {
     constexpr bool SCALAR = V <= 2;
+    constexpr int NA = INTER ? (V + 1) / 2 : V;      // angles of an item
+    constexpr int IB = INTER ? 1 : ITEMS;            // second vectors of items
     __shared__ float2 cs[MAX_ANGLES];
     const int half = p.rd / 2;
+    const int slots = half / NA;                     // rotated items of a row
     const int64_t t0 = blockIdx.x * (int64_t)p.tokens;
     const int nt = (int)min((int64_t)p.tokens, p.T - t0);
+    const int sub = threadIdx.x % LPR, grp = threadIdx.x / LPR;
+    const int t = grp / p.per_token, g = grp - t * p.per_token;
+    // padding: the output rows stay as they are
+    const bool live = t < nt && p.position[t0 + min(t, nt - 1)] >= 0;
+
+    // items: the rotated pairs first (or, interleaved, every vector in order), then the rest
+    const int pairs = INTER ? 0 : half / V, n_items = p.D / V - pairs;
+    int col[ITEMS];
+    bool turn[ITEMS], have[ITEMS];
+#pragma unroll
+    for (int i = 0; i < ITEMS; ++i) {
+        const int item = sub + i * LPR;
+        have[i] = live && item < n_items;
+        const int rest = (item - pairs) * V;
+        col[i] = item < pairs ? p.ro + item * V : (INTER || rest < p.ro ? rest : rest + p.rd);
+        turn[i] = have[i] && (INTER ? col[i] >= p.ro && col[i] < p.ro + p.rd : item < pairs);
+    }
+    // The groups of a warp take the same turns, so that the shuffles need no masks of their own (shuffles under
+    // masks that differ from lane to lane are serialised: 36 us instead of SHFL_US for 8192 tokens of 40 rows).
+    const int first = blockIdx.y * p.per_token, step = gridDim.y * p.per_token;
+    Vec<T, V> xa[ITEMS], xb[IB];
+    auto fetch = [&](const Side &s, int h) {
+        if (h >= s.heads) return;
+        const T *src = static_cast<const T *>(s.x) + (t0 + t) * s.token_stride + h * s.head_stride;
+#pragma unroll
+        for (int i = 0; i < ITEMS; ++i) {
+            if (have[i]) xa[i] = load_vec<T, V, SCALAR>(src + col[i]);
+            if constexpr (!INTER)
+                if (turn[i]) xb[i] = load_vec<T, V, SCALAR>(src + col[i] + half);
+        }
+    };
+    fetch(p.q, first + g);     // on its way while the angles are computed
+
+    // angle i = slot * NA + j of token t sits at (t * NA + j) * slots + slot
     for (int i = threadIdx.x; i < nt * half; i += THREADS) {
-        const int t = i / half;
-        const double turns = (double)p.position[t0 + t] * (double)p.inv_freq[i - t * half] * 0.15915494309189533577;
+        const int t = i / half, a = i - t * half, slot = a / NA, j = a - slot * NA;
+        const double turns = (double)p.position[t0 + t] * (double)p.inv_freq[a] * 0.15915494309189533577;
         float s, c;
         sincospif((float)(2.0 * (turns - rint(turns))), &s, &c);
-        cs[i] = make_float2(c, s);
+        cs[(t * NA + j) * slots + slot] = make_float2(c, s);
     }
     __syncthreads();
 
-    const int sub = threadIdx.x % LPR, grp = threadIdx.x / LPR;
-    constexpr int GROUPS = THREADS / LPR;
-    const int heads = p.q.heads + p.k.heads, rows = nt * heads;
-    // items: the rotated pairs first (half / V of them, or rd / V interleaved vectors), then the rest
-    const int pairs = INTER ? 0 : half / V, n_items = p.D / V - pairs;
-    for (int r0 = blockIdx.y * GROUPS; r0 < rows; r0 += p.row_blocks * GROUPS) {
-        const int r = r0 + grp;
-        // every lane of the warp takes part in the shuffles below
-        const bool live = r < rows;
-        const int t = live ? r / heads : 0, hh = live ? r - t * heads : 0;
-        const bool is_q = hh < p.q.heads;
-        const Side &s = is_q ? p.q : p.k;
-        const int h = is_q ? hh : hh - p.q.heads;
-        const bool skip = !live || p.position[t0 + t] < 0;     // padding: the output row stays as it is
-        const T *src = static_cast<const T *>(s.x) + (t0 + t) * s.token_stride + h * s.head_stride;
-        T *dst = static_cast<T *>(s.out) + (t0 + t) * s.out_token_stride + h * s.out_head_stride;
-        float a[ITEMS][V], b[INTER ? 1 : ITEMS][V];
-        float sum = 0.f;
-        auto first_col = [&](int item) { return item < pairs ? p.ro + item * V : (item - pairs) * V; };
-        // outside the rotated columns: vectors are numbered over the whole row, skipping the rotation's
-        auto plain_col = [&](int item) {
-            const int c = (item - pairs) * V;
-            return INTER || c < p.ro ? c : c + p.rd;
-        };
+    auto walk = [&](const Side &s, bool fetched) {
+        if (first >= s.heads) return;
+        if (!fetched) fetch(s, first + g);
+        const int nw = s.norm_width;
+        // column c takes part in the norm; a vector does as a whole where V > 2
+        auto normed = [&](int c) { return c < nw; };
+        float Pa[ITEMS][V], Qa[ITEMS][V], Pb[IB][V], Qb[IB][V];
 #pragma unroll
         for (int i = 0; i < ITEMS; ++i) {
-            const int item = sub + i * LPR;
-            if (skip || item >= n_items) continue;
-            const bool pair = !INTER && item < pairs;
-            const int c = pair ? first_col(item) : plain_col(item);
-            const Vec<T, V> x = load_vec<T, V, SCALAR>(src + c);
+            const T *w = static_cast<const T *>(s.w);
+            float wa[V], wb[V];
 #pragma unroll
-            for (int j = 0; j < V; ++j) {
-                a[i][j] = to_f32(x.v[j]);
-                if (c + j < s.norm_width) sum += a[i][j] * a[i][j];
-            }
-            if constexpr (!INTER) {
-                if (pair) {
-                    const Vec<T, V> y = load_vec<T, V, SCALAR>(src + c + half);
-#pragma unroll
-                    for (int j = 0; j < V; ++j) {
-                        b[i][j] = to_f32(y.v[j]);
-                        if (c + half + j < s.norm_width) sum += b[i][j] * b[i][j];
-                    }
-                }
-            }
-        }
-#pragma unroll
-        for (int o = LPR / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        if (skip) continue;
-        const float rms = s.norm_width > 0 ? 1.f / sqrtf(sum / s.norm_width + p.eps) : 1.f;
-        const T *w = static_cast<const T *>(s.w);
-        auto normed = [&](float x, int c) {
-            if (c >= s.norm_width) return x;
-            return w ? x * rms * to_f32(w[c]) : x * rms;
-        };
-#pragma unroll
-        for (int i = 0; i < ITEMS; ++i) {
-            const int item = sub + i * LPR;
-            if (item >= n_items) continue;
-            const bool pair = !INTER && item < pairs;
-            const int c = pair ? first_col(item) : plain_col(item);
-#pragma unroll
-            for (int j = 0; j < V; ++j) a[i][j] = normed(a[i][j], c + j);
-            Vec<T, V> o;
-            if constexpr (INTER) {
-                if (c >= p.ro && c < p.ro + p.rd) {
-#pragma unroll
-                    for (int j = 0; j + 1 < V; j += 2) {
-                        const float2 f = cs[t * half + (c - p.ro + j) / 2];
-                        const float u = a[i][j], v = a[i][j + 1];
-                        a[i][j] = u * f.x - v * f.y;
-                        a[i][j + 1] = v * f.x + u * f.y;
-                    }
-                }
-            } else if (pair) {
-                Vec<T, V> o2;
+            for (int j = 0; j < V; ++j) wa[j] = wb[j] = 1.f;
+            if constexpr (SCALAR) {
 #pragma unroll
                 for (int j = 0; j < V; ++j) {
-                    const float2 f = cs[t * half + item * V + j];
-                    const float u = a[i][j], v = normed(b[i][j], c + half + j);
-                    a[i][j] = u * f.x - v * f.y;
-                    o2.v[j] = from_f32<T>(v * f.x + u * f.y);
+                    if (w && have[i] && normed(col[i] + j)) wa[j] = to_f32(w[col[i] + j]);
+                    if (!INTER && w && turn[i] && normed(col[i] + half + j)) wb[j] = to_f32(w[col[i] + half + j]);
                 }
-                store_vec<T, V, SCALAR>(dst + c + half, o2);
+            } else {
+                if (w && have[i] && normed(col[i])) widen(load_vec<T, V, false>(w + col[i]), wa);
+                if (!INTER && w && turn[i] && normed(col[i] + half)) widen(load_vec<T, V, false>(w + col[i] + half), wb);
             }
+            const int slot = INTER ? (col[i] - p.ro) / V : sub + i * LPR;
 #pragma unroll
-            for (int j = 0; j < V; ++j) o.v[j] = from_f32<T>(a[i][j]);
-            store_vec<T, V, SCALAR>(dst + c, o);
+            for (int j = 0; j < NA; ++j) {
+                const float2 f = turn[i] ? cs[(t * NA + j) * slots + slot] : make_float2(1.f, 0.f);
+                if constexpr (INTER) {
+                    Pa[i][2 * j] = wa[2 * j] * f.x;
+                    Qa[i][2 * j] = -wa[2 * j + 1] * f.y;
+                    Pa[i][2 * j + 1] = wa[2 * j + 1] * f.x;
+                    Qa[i][2 * j + 1] = wa[2 * j] * f.y;
+                } else {
+                    Pa[i][j] = wa[j] * f.x;
+                    Qa[i][j] = -wb[j] * f.y;
+                    Pb[i][j] = wb[j] * f.x;
+                    Qb[i][j] = wa[j] * f.y;
+                }
+            }
         }
-    }
+        T *dst = static_cast<T *>(s.out) + (t0 + t) * s.out_token_stride + (first + g) * s.out_head_stride;
+#pragma unroll 1
+        for (int h0 = first; h0 < s.heads; h0 += step, dst += step * s.out_head_stride) {
+            float a[ITEMS][V], b[IB][V];
+            float sum = 0.f;
+#pragma unroll
+            for (int i = 0; i < ITEMS; ++i) {
+                widen(xa[i], a[i]);
+                if constexpr (!INTER) widen(xb[i], b[i]);
+                if (have[i] && (SCALAR || normed(col[i])))
+#pragma unroll
+                    for (int j = 0; j < V; ++j)
+                        if (!SCALAR || normed(col[i] + j)) sum += a[i][j] * a[i][j];
+                if constexpr (!INTER)
+                    if (turn[i] && (SCALAR || normed(col[i] + half)))
+#pragma unroll
+                        for (int j = 0; j < V; ++j)
+                            if (!SCALAR || normed(col[i] + half + j)) sum += b[i][j] * b[i][j];
+            }
+            fetch(s, h0 + step + g);
+            float rms = 1.f;
+            if (nw > 0) {
+#pragma unroll
+                for (int o = LPR / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+                rms = rsqrtf(sum * s.inv_width + p.eps);
+            }
+            if (h0 + g >= s.heads) continue;
+#pragma unroll
+            for (int i = 0; i < ITEMS; ++i) {
+                if (!have[i]) continue;
+                const float ra = normed(col[i]) ? rms : 1.f, rb = normed(col[i] + half) ? rms : 1.f;
+                float oa[V];
+#pragma unroll
+                for (int j = 0; j < V; ++j) a[i][j] *= SCALAR && !normed(col[i] + j) ? 1.f : SCALAR ? rms : ra;
+                if constexpr (INTER) {
+#pragma unroll
+                    for (int j = 0; j < V; ++j) oa[j] = turn[i] ? fmaf(a[i][j ^ 1], Qa[i][j], a[i][j] * Pa[i][j]) : a[i][j] * Pa[i][j];
+                } else if (turn[i]) {
+                    float ob[V];
+#pragma unroll
+                    for (int j = 0; j < V; ++j) {
+                        b[i][j] *= SCALAR && !normed(col[i] + half + j) ? 1.f : SCALAR ? rms : rb;
+                        oa[j] = fmaf(b[i][j], Qa[i][j], a[i][j] * Pa[i][j]);
+                        ob[j] = fmaf(a[i][j], Qb[i][j], b[i][j] * Pb[i][j]);
+                    }
+                    store_vec<T, V, SCALAR>(dst + col[i] + half, narrow<T, V>(ob));
+                } else {
+#pragma unroll
+                    for (int j = 0; j < V; ++j) oa[j] = a[i][j] * Pa[i][j];
+                }
+                store_vec<T, V, SCALAR>(dst + col[i], narrow<T, V>(oa));
+            }
+        }
+    };
+    walk(p.q, true);
+    walk(p.k, false);
 }
 
 template <class T, int V, bool INTER>
@@ -177,17 +277,19 @@ static int launch(Params &p, cudaStream_t stream) {
     int lpr = 4;
     while (lpr < 32 && lpr < n_items) lpr *= 2;
     const int items = (n_items + lpr - 1) / lpr;
-    const int heads = p.q.heads + p.k.heads, groups = THREADS / lpr, half = p.rd / 2;
-    // A CTA takes enough tokens to fill its threads with angles, fewer where that leaves the GPU
-    // empty; a single token's rows are dealt over several CTAs when tokens are few.
-    const int ctas = 4 * sm_count();
-    int tokens = max(1, min(half > 0 ? THREADS / half : 8, MAX_ANGLES / max(half, 1)));
-    while (tokens > 1 && (p.T + tokens - 1) / tokens < ctas) tokens /= 2;
-    const int64_t blocks = (p.T + tokens - 1) / tokens;
-    const int passes = (tokens * heads + groups - 1) / groups;
-    p.tokens = tokens;
-    p.row_blocks = (int)max((int64_t)1, min((int64_t)passes, ctas / blocks));
-    const dim3 grid((unsigned)blocks, p.row_blocks);
+    const int heads = max(p.q.heads, p.k.heads), groups = THREADS / lpr, half = p.rd / 2;
+    // Lane groups that fill the GPU (2048 threads a multiprocessor), dealt to the tokens: with many tokens a group
+    // takes many heads of its token, with few the heads are spread over groups and CTAs.  (8192 tokens of 40
+    // rows: 36.5 us; groups for 4096 or 1024 threads: 46 and 48; CTAs of 256: 39; 7 or 8 CTAs a
+    // multiprocessor, which spill: 39 and 43.)
+    const int64_t all = (int64_t)sm_count() * 2048 / lpr;
+    int64_t want = lsa_max64(1, lsa_min64(heads, all / lsa_max64(p.T, 1)));
+    int per_token = 1;
+    while (per_token < groups && per_token < want) per_token *= 2;
+    while (half > 0 && groups / per_token * half > MAX_ANGLES && per_token < groups) per_token *= 2;
+    p.per_token = per_token;
+    p.tokens = groups / per_token;
+    const dim3 grid((unsigned)((p.T + p.tokens - 1) / p.tokens), (unsigned)((want + per_token - 1) / per_token));
 #define LSA_ROPE(L, I) norm_rope_kernel<T, V, L, I, INTER><<<grid, THREADS, 0, stream>>>(p)
     constexpr int MOST = 1024 / V / 32;   // items a lane of the widest row can have
     if (items == 1) {
@@ -249,16 +351,16 @@ extern "C" int lsa_qk_norm_rope(int dtype, int64_t T, int head_dim, const void *
                 LSA_ERR_INVALID_ARG, "lsa_qk_norm_rope: a pointer is not aligned to its element type");
     if (T == 0) return LSA_OK;
     rope::Params p = {};
-    p.q = {q, q_out, q_weight, q_token_stride, q_head_stride, q_out_token_stride, q_out_head_stride, Hq, q_norm_width};
-    p.k = {k, k_out, k_weight, k_token_stride, k_head_stride, k_out_token_stride, k_out_head_stride, Hk, k_norm_width};
+    p.q = {q, q_out, q_weight, q_token_stride, q_head_stride, q_out_token_stride, q_out_head_stride, Hq, q_norm_width, q_norm_width ? 1.f / q_norm_width : 0.f};
+    p.k = {k, k_out, k_weight, k_token_stride, k_head_stride, k_out_token_stride, k_out_head_stride, Hk, k_norm_width, k_norm_width ? 1.f / k_norm_width : 0.f};
     p.position = position; p.inv_freq = inv_freq; p.T = T; p.D = head_dim; p.ro = rot_offset; p.rd = rot_dim; p.eps = eps;
-    // The widest vector (up to 16 bytes) that divides the row, the rotation's bounds, and every
-    // row's address.
+    // The widest vector (up to 16 bytes) that divides the row, the rotation's and norms' bounds, and
+    // every row's address.
     const int64_t full = 16 / size, unit = interleaved ? 1 : rot_dim / 2;
     int64_t bits = head_dim | rot_offset | (interleaved ? rot_dim : unit);
     for (const rope::Side *s : {&p.q, &p.k})
         if (s->heads)
-            bits |= s->token_stride | s->head_stride | s->out_token_stride | s->out_head_stride |
+            bits |= s->norm_width | (int64_t)(reinterpret_cast<uintptr_t>(s->w) / size) | s->token_stride | s->head_stride | s->out_token_stride | s->out_head_stride |
                     (int64_t)(reinterpret_cast<uintptr_t>(s->x) / size) | (int64_t)(reinterpret_cast<uintptr_t>(s->out) / size);
     int64_t vec = full;
     while (vec > 1 && bits % vec) vec /= 2;

@@ -60,46 +60,53 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
     return d;
 }
 
-// The 16 values of one group as 8 code bytes and the e4m3 scale byte.
+// Half a group: eight values as four code bytes and, in scale_byte, the scale of the whole group, whose other half
+// is with the neighbouring lane (lane ^ 1; both call together).
 //   s = e4m3(min(amax / (6 g), 448)),  code = e2m1(x / (s g)), both to nearest even and
-//   saturating; s = 0 stores zeros.  amax / 6 and x / s often lie exactly halfway between two
-//   codes, so both quotients are true (correctly rounded) divisions, never products with a
-//   rounded reciprocal.  A NaN in the group gives a NaN scale: the whole group reads as NaN.
+//   saturating; s = 0 stores zeros.  A NaN in the group gives a NaN scale: the whole group reads as NaN.
 //   An infinity saturates the scale; the finite values of its group then read as they round.
-__device__ __forceinline__ uint2 quantise_group(const float (&x)[16], float g, float g6, uint32_t &scale_byte) {
+// amax / 6 and x / s often lie exactly halfway between two codes, so a product with a rounded
+// reciprocal will not do.  EXACT divides.  Otherwise (x of at most 11 significant bits, g a power of
+// two, so s g has 4): a quotient X / S 2^k that is not the halfway point T 2^m (T <= 7) is off it by at
+// least 2^-11 of its size, because X 2^a and S T are whole numbers below 2^11 when both are scaled to the
+// same size; so the product with the reciprocal, off by 2^-23 at most, is rounded to 16
+// significant bits, which brings the halfway points back and moves nothing else across one.
+template <bool EXACT>
+__device__ __forceinline__ uint32_t quantise_half(const float (&x)[8], float g, float g6, uint32_t &scale_byte) {
     float amax = 0.f;
     bool nan = false;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
+    for (int i = 0; i < 8; ++i) {
         amax = fmaxf(amax, fabsf(x[i]));
         nan |= x[i] != x[i];
     }
+    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+    nan |= __shfl_xor_sync(0xffffffffu, (int)nan, 1) != 0;
     const float t = fminf(__fdiv_rn(amax, g6), E4M3_MAX);
     uint16_t e;
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(e) : "f"(0.f), "f"(t));
-    const uint32_t sh = e4m3x2_to_f16(e);
-    const float sg = __half2float(__ushort_as_half((uint16_t)sh)) * g;
+    const float sg = __half2float(__ushort_as_half((uint16_t)e4m3x2_to_f16(e))) * g;
     scale_byte = nan ? 0x7fu : (e & 0xffu);
-    uint2 codes = make_uint2(0u, 0u);
-    if (sg > 0.f) {
-        uint32_t w[2];
+    if (!(sg > 0.f)) return 0u;
+    float y[8];
+    if constexpr (EXACT) {
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            float y[8];
+        for (int i = 0; i < 8; ++i) y[i] = __fdiv_rn(x[i], sg);
+    } else {
+        const float r = __fdiv_rn(1.f, sg);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) y[i] = __fdiv_rn(x[8 * j + i], sg);
-            asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
-                "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\t"
-                "cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n\t"
-                "cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n\t"
-                "cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n\t"
-                "mov.b32 %0, {b0, b1, b2, b3};\n\t}"
-                : "=r"(w[j])
-                : "f"(y[0]), "f"(y[1]), "f"(y[2]), "f"(y[3]), "f"(y[4]), "f"(y[5]), "f"(y[6]), "f"(y[7]));
-        }
-        codes = make_uint2(w[0], w[1]);
+        for (int i = 0; i < 8; ++i) y[i] = __uint_as_float((__float_as_uint(x[i] * r) + 0x40u) & ~0x7fu);
     }
-    return codes;
+    uint32_t w;
+    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n\t"
+        "mov.b32 %0, {b0, b1, b2, b3};\n\t}"
+        : "=r"(w)
+        : "f"(y[0]), "f"(y[1]), "f"(y[2]), "f"(y[3]), "f"(y[4]), "f"(y[5]), "f"(y[6]), "f"(y[7]));
+    return w;
 }
 
 }  // namespace q4

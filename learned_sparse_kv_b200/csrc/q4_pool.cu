@@ -2,11 +2,13 @@
 // (prefill and decode batches) or to the end of the recent window (one decoded token per
 // sequence), and the read back.
 //
-// One thread owns one group of 16 values: its maximum, its scale, its 8 code bytes and its
-// scale byte need no other thread, and consecutive threads touch consecutive memory.  Bound
-// by memory: 2 + 0.5625 bytes a bf16 value.
+// A thread owns half a group, eight values: 16 bytes of a bf16 row, 4 code bytes; the two lanes of a
+// group exchange their maxima.  A thread keeps its place in the row (side, head, columns) and walks
+// the tokens, so that no division is left in the loop.  Bound by memory: 2 + 0.5625 bytes a bf16 value.
 #include "nvtx_range.cuh"
 #include "q4.cuh"
+
+#include <math.h>
 
 namespace lsa {
 
@@ -19,44 +21,77 @@ struct Q4Side {
     float g, g6;
 };
 
-// Quantises group `grp` of row (t, h) into pool row `slot` (slot * 64 + row in the chunk).
+// A thread's place: half group u of a token's rows (K's first, then V's).
+struct Place {
+    const Q4Side &s;
+    int h, col;          // head, first of the eight columns
+    __device__ Place(const Q4Side &a, const Q4Side &b, int u, int per_a) : s(u < per_a ? a : b) {
+        if (u >= per_a) u -= per_a;
+        const int halves = s.W / 8;
+        h = u / halves;
+        col = (u - h * halves) * 8;
+    }
+};
+
 template <class T>
-__device__ __forceinline__ void write_group(const Q4Side &s, int heads, int64_t t, int h, int grp, int64_t slot) {
-    const T *src = static_cast<const T *>(s.x) + t * s.token_stride + h * s.head_stride + grp * q4::GROUP;
-    float x[16];
+__device__ __forceinline__ void load8(const T *src, float (&x)[8]) {
     constexpr int PER = 16 / sizeof(T);
 #pragma unroll
-    for (int i = 0; i < 16 / PER; ++i) {
+    for (int i = 0; i < 8 / PER; ++i) {
         const Vec<T, PER> v = *reinterpret_cast<const Vec<T, PER> *>(src + i * PER);
 #pragma unroll
         for (int j = 0; j < PER; ++j) x[i * PER + j] = to_f32(v.v[j]);
     }
-    uint32_t sb;
-    const uint2 codes = q4::quantise_group(x, s.g, s.g6, sb);
-    uint8_t *chunk = s.pool + ((slot / LSA_CHUNK) * heads + h) * q4::chunk_bytes(s.W);
-    const int r = (int)(slot % LSA_CHUNK);
-    *reinterpret_cast<uint2 *>(chunk + r * q4::code_row(s.W) + grp * 8) = codes;
-    chunk[q4::scale_base(s.W) + r * q4::scale_row(s.W) + grp] = (uint8_t)sb;
 }
 
-// grid-stride over (token, side, head, group); `per` groups a token over both sides.
-template <class T>
-__global__ void __launch_bounds__(256) q4_write_kernel(const Q4Side a, const Q4Side b, int heads, int64_t n, int per,
+// The whole warp calls; slot < 0: nothing is written.
+template <bool EXACT>
+__device__ __forceinline__ void put_half(const Place &at, int heads, int64_t slot, const float (&x)[8]) {
+    const Q4Side &s = at.s;
+    uint32_t sb;
+    const uint32_t codes = q4::quantise_half<EXACT>(x, s.g, s.g6, sb);
+    if (slot < 0) return;
+    uint8_t *chunk = s.pool + ((slot / LSA_CHUNK) * heads + at.h) * q4::chunk_bytes(s.W);
+    const int r = (int)(slot % LSA_CHUNK);
+    *reinterpret_cast<uint32_t *>(chunk + r * q4::code_row(s.W) + at.col / 2) = codes;
+    if (!(at.col & 8)) chunk[q4::scale_base(s.W) + r * q4::scale_row(s.W) + at.col / 16] = (uint8_t)sb;
+}
+
+// `per` half groups a token; where they are fewer than the block's threads, a block takes several tokens at once.
+template <class T, bool EXACT>
+__global__ void __launch_bounds__(256) q4_write_kernel(const Q4Side a, const Q4Side b, int heads, int64_t T_, int per,
                                                        int per_a, int64_t n_rows, const int64_t *__restrict__ slot_map,
                                                        int32_t *status) {
-    for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < n; i += gridDim.x * 256ll) {
-        const int64_t t = i / per;
-        int u = (int)(i - t * per);
-        const int64_t slot = slot_map[t];
-        if (slot < 0 || slot >= n_rows) {
-            if (slot != -1) flag(status, LSA_DEV_INDEX);
-            continue;
+    // The loops are the same for every thread of a block: lanes exchange their maxima.
+    const int tokens = max(1, 256 / per), mine = per < 256 ? (int)threadIdx.x / per : 0;
+    for (int u0 = 0; u0 < per; u0 += 256) {
+        const int u = u0 + (int)threadIdx.x - mine * per;
+        const bool live = mine < tokens && u < per;
+        const Place at(a, b, live ? u : 0, per_a);
+        const T *src = static_cast<const T *>(at.s.x) + at.h * at.s.head_stride + at.col;
+        const int64_t step = (int64_t)gridDim.x * tokens;
+        for (int64_t t0 = (int64_t)blockIdx.x * tokens; t0 < T_; t0 += 2 * step) {
+            // two tokens in flight
+            float x[2][8];
+            int64_t slot[2];
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+                const int64_t t = t0 + mine + n * step;
+                slot[n] = -1;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) x[n][j] = 0.f;
+                if (live && t < T_) {
+                    slot[n] = slot_map[t];
+                    load8(src + t * at.s.token_stride, x[n]);
+                }
+            }
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+                const bool there = slot[n] >= 0 && slot[n] < n_rows;
+                if (!there && slot[n] != -1) flag(status, LSA_DEV_INDEX);
+                put_half<EXACT>(at, heads, there ? slot[n] : -1, x[n]);
+            }
         }
-        const bool first = u < per_a;
-        if (!first) u -= per_a;
-        const Q4Side &s = first ? a : b;
-        const int groups = s.W / q4::GROUP, h = u / groups;
-        write_group<T>(s, heads, t, h, u - h * groups, slot);
     }
 }
 
@@ -80,11 +115,13 @@ __global__ void __launch_bounds__(256) q4_append_kernel(const Q4Side a, const Q4
     __syncthreads();
     const int64_t row = s_row;
     if (row < 0) return;
-    for (int i = threadIdx.x; i < per; i += 256) {
-        const bool first = i < per_a;
-        const Q4Side &s = first ? a : b;
-        const int u = first ? i : i - per_a, groups = s.W / q4::GROUP, h = u / groups;
-        write_group<T>(s, heads, seq, h, u - h * groups, row);
+    for (int u0 = 0; u0 < per; u0 += 256) {
+        const int u = u0 + (int)threadIdx.x;
+        const bool live = u < per;
+        const Place at(a, b, live ? u : 0, per_a);
+        float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        if (live) load8(static_cast<const T *>(at.s.x) + seq * at.s.token_stride + at.h * at.s.head_stride + at.col, x);
+        put_half<true>(at, heads, live ? row : -1, x);
     }
     if (li_pool)
         for (int c = threadIdx.x; c < dl / 8; c += 256)
@@ -94,50 +131,70 @@ __global__ void __launch_bounds__(256) q4_append_kernel(const Q4Side a, const Q4
 
 template <class T>
 __global__ void __launch_bounds__(256) q4_read_kernel(const uint8_t *__restrict__ pool, int heads, int W, int64_t n_rows,
-                                                      const int64_t *__restrict__ slot_map, int64_t n, float g,
+                                                      const int64_t *__restrict__ slot_map, int64_t T_, float g,
                                                       T *__restrict__ out, int32_t *status) {
-    const int groups = W / q4::GROUP, per = heads * groups;
-    for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < n; i += gridDim.x * 256ll) {
-        const int64_t t = i / per;
-        const int u = (int)(i - t * per), h = u / groups, grp = u - h * groups;
-        const int64_t slot = slot_map[t];
-        const bool there = slot >= 0 && slot < n_rows;
-        uint2 codes = make_uint2(0u, 0u);
-        float s = 0.f;
-        if (there) {
-            const uint8_t *chunk = pool + ((slot / LSA_CHUNK) * heads + h) * q4::chunk_bytes(W);
-            const int r = (int)(slot % LSA_CHUNK);
-            codes = *reinterpret_cast<const uint2 *>(chunk + r * q4::code_row(W) + grp * 8);
-            const uint32_t sh = q4::e4m3x2_to_f16(chunk[q4::scale_base(W) + r * q4::scale_row(W) + grp]);
-            s = __half2float(__ushort_as_half((uint16_t)sh));
-        } else if (slot != -1) {
-            flag(status, LSA_DEV_INDEX);
-        }
-        float x[16];
+    const int halves = W / 8, per = heads * halves;
+    const int tokens = max(1, 256 / per), mine = (int)threadIdx.x / per;
+    if (per < 256 && mine >= tokens) return;
+    for (int u = per < 256 ? threadIdx.x - mine * per : threadIdx.x; u < per; u += 256) {
+        const int h = u / halves, col = (u - h * halves) * 8;
+        const uint8_t *base = pool + h * q4::chunk_bytes(W);
+        const int64_t step = (int64_t)gridDim.x * tokens;
+        for (int64_t t = (int64_t)blockIdx.x * tokens + (per < 256 ? mine : 0); t < T_; t += 4 * step) {
+            // four tokens in flight
+            int64_t slot[4];
+            uint32_t codes[4], sb[4];
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            uint32_t p[4];
-            q4::e2m1x8_to_f16(j ? codes.y : codes.x, p);
+            for (int n = 0; n < 4; ++n) slot[n] = t + n * step < T_ ? slot_map[t + n * step] : -2;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&p[k]));
-                x[8 * j + 2 * k] = f.x * s * g;        // e2m1 * e4m3 is exact: one rounding, with g
-                x[8 * j + 2 * k + 1] = f.y * s * g;
+            for (int n = 0; n < 4; ++n) {
+                codes[n] = sb[n] = 0u;
+                if (slot[n] >= 0 && slot[n] < n_rows) {
+                    const uint8_t *chunk = base + (slot[n] / LSA_CHUNK) * heads * q4::chunk_bytes(W);
+                    const int r = (int)(slot[n] % LSA_CHUNK);
+                    codes[n] = *reinterpret_cast<const uint32_t *>(chunk + r * q4::code_row(W) + col / 2);
+                    sb[n] = chunk[q4::scale_base(W) + r * q4::scale_row(W) + col / 16];
+                }
             }
-        }
-        constexpr int PER = 16 / sizeof(T);
-        T *dst = out + i * q4::GROUP;
 #pragma unroll
-        for (int k = 0; k < 16 / PER; ++k) {
-            Vec<T, PER> v;
+            for (int n = 0; n < 4; ++n) {
+                if (t + n * step >= T_) break;
+                if (slot[n] < -1 || slot[n] >= n_rows) flag(status, LSA_DEV_INDEX);
+                uint32_t p[4];
+                q4::e2m1x8_to_f16(codes[n], p);
+                const uint32_t s = q4::dup_lo(q4::e4m3x2_to_f16(sb[n]));
+                float x[8];
 #pragma unroll
-            for (int j = 0; j < PER; ++j) v.v[j] = from_f32<T>(x[k * PER + j]);
-            *reinterpret_cast<Vec<T, PER> *>(dst + k * PER) = v;
+                for (int k = 0; k < 4; ++k) {
+                    const uint32_t v = q4::hmul2(p[k], s);     // exact: one rounding, with g
+                    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&v));
+                    x[2 * k] = f.x * g;
+                    x[2 * k + 1] = f.y * g;
+                }
+                constexpr int PER = 16 / sizeof(T);
+                T *dst = out + ((t + n * step) * per + u) * 8;
+#pragma unroll
+                for (int k = 0; k < 8 / PER; ++k) {
+                    Vec<T, PER> v;
+#pragma unroll
+                    for (int j = 0; j < PER; ++j) v.v[j] = from_f32<T>(x[k * PER + j]);
+                    *reinterpret_cast<Vec<T, PER> *>(dst + k * PER) = v;
+                }
+            }
         }
     }
 }
 
-static int q4_blocks(int64_t n) { return (int)lsa_min64((n + 255) / 256, (int64_t)sm_count() * 16); }
+// Blocks for T tokens of `per` half groups, `flight` tokens of a thread at a time: up to 16 a multiprocessor.
+static int q4_blocks(int64_t T, int per, int flight) {
+    const int64_t tokens = per < 256 ? 256 / per : 1;
+    return (int)lsa_max64(1, lsa_min64((T + tokens * flight - 1) / (tokens * flight), (int64_t)sm_count() * 16));
+}
+
+static bool power_of_two(float g) {
+    int e;
+    return frexpf(g, &e) == 0.5f;
+}
 
 static bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
@@ -180,15 +237,18 @@ extern "C" int lsa_write_q4(int dtype, int64_t T, int heads, const void *k, int6
     LSA_REQUIRE(two || !v, LSA_ERR_INVALID_ARG, "lsa_write_q4: v without a v_pool");
     LSA_REQUIRE(slot_map || T == 0, LSA_ERR_INVALID_ARG, "lsa_write_q4: null pointer (slot_map)");
     if (T == 0) return LSA_OK;
-    const int per_a = heads * (a.W / 16), per = per_a + (two ? heads * (b.W / 16) : 0);
-    const int64_t n = T * per, rows = n_slots * LSA_CHUNK;
-    const int blocks = q4_blocks(n);
-    if (dtype == LSA_DTYPE_BF16)
-        q4_write_kernel<__nv_bfloat16><<<blocks, 256, 0, stream>>>(a, b, heads, n, per, per_a, rows, slot_map, dev_status);
-    else if (dtype == LSA_DTYPE_F16)
-        q4_write_kernel<__half><<<blocks, 256, 0, stream>>>(a, b, heads, n, per, per_a, rows, slot_map, dev_status);
-    else
-        q4_write_kernel<float><<<blocks, 256, 0, stream>>>(a, b, heads, n, per, per_a, rows, slot_map, dev_status);
+    const int per_a = heads * (a.W / 8), per = per_a + (two ? heads * (b.W / 8) : 0);
+    const int64_t rows = n_slots * LSA_CHUNK;
+    // 16-bit rows and power-of-two scales need no division (quantise_half): 16384 tokens, 8 heads, K and V
+    const bool exact = dtype == LSA_DTYPE_F32 || !power_of_two(k_scale) || (two && !power_of_two(v_scale));
+    const int blocks = q4_blocks(T, per, 2);
+#define LSA_WRITE(TYPE, E) q4_write_kernel<TYPE, E><<<blocks, 256, 0, stream>>>(a, b, heads, T, per, per_a, rows, slot_map, dev_status)
+    if (dtype == LSA_DTYPE_F32) LSA_WRITE(float, true);
+    else if (dtype == LSA_DTYPE_BF16 && exact) LSA_WRITE(__nv_bfloat16, true);
+    else if (dtype == LSA_DTYPE_BF16) LSA_WRITE(__nv_bfloat16, false);
+    else if (exact) LSA_WRITE(__half, true);
+    else LSA_WRITE(__half, false);
+#undef LSA_WRITE
     return check_launch("q4_write_kernel");
 }
 
@@ -214,7 +274,7 @@ extern "C" int lsa_append_token_q4(int dtype, int heads, const void *new_k, int 
                     (!li_pool || (dl >= 8 && dl % 8 == 0 && aligned16(new_li) && aligned16(li_pool))),
                 LSA_ERR_INVALID_ARG,
                 "lsa_append_token_q4: new_li and li_pool come together, 16-byte aligned, dl a multiple of 8");
-    const int per_a = heads * (a.W / 16), per = per_a + (two ? heads * (b.W / 16) : 0);
+    const int per_a = heads * (a.W / 8), per = per_a + (two ? heads * (b.W / 8) : 0);
     if (dtype == LSA_DTYPE_BF16)
         q4_append_kernel<__nv_bfloat16><<<B, 256, 0, stream>>>(a, b, heads, per, per_a, new_li, li_pool, dl, n_slots, chunk_table, table_stride, window_start, window_len, dev_status);
     else if (dtype == LSA_DTYPE_F16)
@@ -239,13 +299,13 @@ extern "C" int lsa_read_q4(const uint8_t *pool, int64_t n_slots, int heads, int 
     LSA_REQUIRE(scale > 0.f && scale <= 1e30f && scale >= 1e-30f, LSA_ERR_INVALID_ARG,
                 "lsa_read_q4: the pool scale must be positive and between 1e-30 and 1e30");
     if (T == 0) return LSA_OK;
-    const int64_t n = T * heads * (width / 16), rows = n_slots * LSA_CHUNK;
-    const int blocks = q4_blocks(n);
+    const int64_t rows = n_slots * LSA_CHUNK;
+    const int blocks = q4_blocks(T, heads * (width / 8), 4);
     if (out_dtype == LSA_DTYPE_BF16)
-        q4_read_kernel<<<blocks, 256, 0, stream>>>(pool, heads, width, rows, slot_map, n, scale, static_cast<__nv_bfloat16 *>(out), dev_status);
+        q4_read_kernel<<<blocks, 256, 0, stream>>>(pool, heads, width, rows, slot_map, T, scale, static_cast<__nv_bfloat16 *>(out), dev_status);
     else if (out_dtype == LSA_DTYPE_F16)
-        q4_read_kernel<<<blocks, 256, 0, stream>>>(pool, heads, width, rows, slot_map, n, scale, static_cast<__half *>(out), dev_status);
+        q4_read_kernel<<<blocks, 256, 0, stream>>>(pool, heads, width, rows, slot_map, T, scale, static_cast<__half *>(out), dev_status);
     else
-        q4_read_kernel<<<blocks, 256, 0, stream>>>(pool, heads, width, rows, slot_map, n, scale, static_cast<float *>(out), dev_status);
+        q4_read_kernel<<<blocks, 256, 0, stream>>>(pool, heads, width, rows, slot_map, T, scale, static_cast<float *>(out), dev_status);
     return check_launch("q4_read_kernel");
 }

@@ -7,6 +7,7 @@ and turns a non-zero status into an LSAError.  There is no CPU fallback: if
 the library is missing the import fails.
 """
 import ctypes
+import functools
 import os
 
 import torch
@@ -492,18 +493,23 @@ class _NoSwitch:
 _NO_SWITCH = _NoSwitch()
 
 
+# torch's own short cut to the current stream's handle (no Stream object), where this torch has it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def _on(index):
     """Makes device `index` current for the call, if it is not."""
     return _NO_SWITCH if torch.cuda.current_device() == index else torch.cuda.device(index)
 
 
 def _handle(index, stream):
-    return stream.cuda_stream if stream is not None else torch.cuda.current_stream(index).cuda_stream
+    return _raw_stream(index) if stream is None else stream.cuda_stream
 
 
-def _workspace(nbytes, ws, index):
+def _workspace(nbytes, ws, dev, index):
     if ws is None:
-        return torch.empty(nbytes if nbytes > 256 else 256, dtype=_U8, device=torch.device("cuda", index))
+        return torch.empty(nbytes if nbytes > 256 else 256, dtype=_U8, device=dev)
     if not (ws.dtype is _U8 and ws.is_cuda and ws.get_device() == index and ws.is_contiguous()):
         raise LSAError(1, f"ws must be a contiguous uint8 tensor on cuda:{index}")
     return ws
@@ -516,6 +522,7 @@ def _side(stream, index, *fresh):
             t.record_stream(stream)
 
 
+@functools.lru_cache(maxsize=256)
 def build_tables_workspace_size(B, table_stride, n_slots):
     return _lib.lsa_build_tables_workspace_size(B, table_stride, n_slots)
 
@@ -538,13 +545,15 @@ def build_tables(table, cached_len, new_len, n_slots, max_new, *, table_next=Non
             table_next = torch.empty_like(table)
         if slot_map is None:
             slot_map = torch.empty(max_new, dtype=_I64, device=dev)
+        if position is None and new_offset is None and n_free is None:     # one allocation
+            position, new_offset, n_free = torch.empty(max_new + B + 2, dtype=_I32, device=dev).split((max_new, B + 1, 1))
         if position is None:
             position = torch.empty(max_new, dtype=_I32, device=dev)
         if new_offset is None:
             new_offset = torch.empty(B + 1, dtype=_I32, device=dev)
         if n_free is None:
             n_free = torch.empty(1, dtype=_I32, device=dev)
-        ws = _workspace(_lib.lsa_build_tables_workspace_size(B, stride, n_slots), ws, index)
+        ws = _workspace(build_tables_workspace_size(B, stride, n_slots), ws, dev, index)
         _check(_lib.lsa_build_tables(
             _arg(table, _I32, (B, stride), index, "table"), stride, _arg(cached_len, _I32, (B,), index, "cached_len"),
             _arg(new_len, _I32, (B,), index, "new_len"), B, n_slots, max_new,
@@ -723,6 +732,7 @@ def read_q4(pool, slot_map, *, scale=1.0, out=None, out_dtype=torch.bfloat16, st
     return out
 
 
+@functools.lru_cache(maxsize=256)
 def sparse_decode_q4_workspace_size(B, Hq, heads, dqk, dv, k, max_window_len):
     return _lib.lsa_sparse_decode_q4_workspace_size(B, Hq, heads, dqk, dv, k, max_window_len)
 
@@ -754,7 +764,7 @@ def sparse_decode_q4(q, k_pool, v_pool, chunk_table, topk_idx, topk_count, windo
             out = torch.empty(B, Hq, dv, dtype=out_dtype, device=dev)
         if lse is None and want_lse:
             lse = torch.empty(B, Hq, dtype=_F32, device=dev)
-        ws = _workspace(_lib.lsa_sparse_decode_q4_workspace_size(B, Hq, heads, dqk, dv, k, max_window_len), ws, index)
+        ws = _workspace(sparse_decode_q4_workspace_size(B, Hq, heads, dqk, dv, k, max_window_len), ws, dev, index)
         _check(_lib.lsa_sparse_decode_q4(
             _dtype(q.dtype, "q"), _arg(q, q.dtype, (B, Hq, dqk), index, "q"),
             _arg(k_pool, _U8, (n_slots, heads, 36 * dqk), index, "k_pool"), k_scale, vpool, v_scale, n_slots, heads,
