@@ -69,54 +69,6 @@ __device__ __forceinline__ void store_vec(T *dst, const Vec<T, V> &v) {
     }
 }
 
-// Pairs of elements: two from a 32-bit word (16-bit types), and back, rounding to nearest even.
-template <class T> struct Two;
-template <> struct Two<__nv_bfloat16> {
-    static __device__ __forceinline__ float2 get(const Vec<__nv_bfloat16, 2> &v) {
-        const uint32_t w = *reinterpret_cast<const uint32_t *>(&v);
-        return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
-    }
-    static __device__ __forceinline__ void put(Vec<__nv_bfloat16, 2> &v, float a, float b) {
-        *reinterpret_cast<uint32_t *>(&v) = pack_bf16x2(a, b);
-    }
-};
-template <> struct Two<__half> {
-    static __device__ __forceinline__ float2 get(const Vec<__half, 2> &v) {
-        return __half22float2(*reinterpret_cast<const __half2 *>(&v));
-    }
-    static __device__ __forceinline__ void put(Vec<__half, 2> &v, float a, float b) {
-        *reinterpret_cast<uint32_t *>(&v) = q4::pack_f16x2(a, b);
-    }
-};
-template <> struct Two<float> {
-    static __device__ __forceinline__ float2 get(const Vec<float, 2> &v) { return make_float2(v.v[0], v.v[1]); }
-    static __device__ __forceinline__ void put(Vec<float, 2> &v, float a, float b) { v.v[0] = a; v.v[1] = b; }
-};
-template <class T, int V>
-__device__ __forceinline__ void widen(const Vec<T, V> &v, float (&x)[V]) {
-    if constexpr (V == 1) {
-        x[0] = to_f32(v.v[0]);
-    } else {
-#pragma unroll
-        for (int j = 0; j < V; j += 2) {
-            const float2 f = Two<T>::get(*reinterpret_cast<const Vec<T, 2> *>(&v.v[j]));
-            x[j] = f.x;
-            x[j + 1] = f.y;
-        }
-    }
-}
-template <class T, int V>
-__device__ __forceinline__ Vec<T, V> narrow(const float (&x)[V]) {
-    Vec<T, V> v;
-    if constexpr (V == 1) {
-        v.v[0] = from_f32<T>(x[0]);
-    } else {
-#pragma unroll
-        for (int j = 0; j < V; j += 2) Two<T>::put(*reinterpret_cast<Vec<T, 2> *>(&v.v[j]), x[j], x[j + 1]);
-    }
-    return v;
-}
-
 // V: elements of a vector; LPR: lanes of a row; ITEMS: items of a lane.  V > 2 divides every bound of the row
 // (rotation, norm widths); V <= 2 moves and checks element by element.
 template <class T, int V, int LPR, int ITEMS, bool INTER>

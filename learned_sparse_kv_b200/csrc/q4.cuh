@@ -60,42 +60,52 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
     return d;
 }
 
+// The larger of two, NaN if either is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float d;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+    return d;
+}
+// The 16 highest significant bits.
+__device__ __forceinline__ float cut16(float x) { return __uint_as_float(__float_as_uint(x) & ~0x7fu); }
+
 // Half a group: eight values as four code bytes and, in scale_byte, the scale of the whole group, whose other half
 // is with the neighbouring lane (lane ^ 1; both call together).
 //   s = e4m3(min(amax / (6 g), 448)),  code = e2m1(x / (s g)), both to nearest even and
 //   saturating; s = 0 stores zeros.  A NaN in the group gives a NaN scale: the whole group reads as NaN.
 //   An infinity saturates the scale; the finite values of its group then read as they round.
 // amax / 6 and x / s often lie exactly halfway between two codes, so a product with a rounded
-// reciprocal will not do.  EXACT divides.  Otherwise (x of at most 11 significant bits, g a power of
-// two, so s g has 4): a quotient X / S 2^k that is not the halfway point T 2^m (T <= 7) is off it by at
-// least 2^-11 of its size, because X 2^a and S T are whole numbers below 2^11 when both are scaled to the
-// same size; so the product with the reciprocal, off by 2^-23 at most, is rounded to 16
-// significant bits, which brings the halfway points back and moves nothing else across one.
+// reciprocal will not do.  EXACT divides.  Otherwise (x of at most 11 significant bits, g a power of two, so
+// s g has 4): a quotient X / S 2^k that is not the halfway point T 2^m is off it by at least 2^-11 of its
+// size, because X 2^a and S T are whole numbers below 2^11 when both are scaled to the same size
+// (T <= 7 and S <= 15 for the codes, T <= 31 and S = 6 for the scale).  The product with the approximate
+// reciprocal is off by less than 2^-21; made larger by 2^-17 and cut to 16 significant bits it is the
+// halfway point again where the quotient is, and nothing else crosses one.
 template <bool EXACT>
 __device__ __forceinline__ uint32_t quantise_half(const float (&x)[8], float g, float g6, uint32_t &scale_byte) {
     float amax = 0.f;
-    bool nan = false;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        amax = fmaxf(amax, fabsf(x[i]));
-        nan |= x[i] != x[i];
-    }
-    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-    nan |= __shfl_xor_sync(0xffffffffu, (int)nan, 1) != 0;
-    const float t = fminf(__fdiv_rn(amax, g6), E4M3_MAX);
+    for (int i = 0; i < 8; ++i) amax = max_nan(amax, fabsf(x[i]));
+    amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+    constexpr float UP = 1.f + 0x1p-17f;
+    float t;
+    if constexpr (EXACT) t = __fdiv_rn(amax, g6);
+    else t = cut16(amax * (UP * g6));           // g6: 1 / (6 g) here
     uint16_t e;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(e) : "f"(0.f), "f"(t));
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(e) : "f"(0.f), "f"(fminf(t, E4M3_MAX)));
     const float sg = __half2float(__ushort_as_half((uint16_t)e4m3x2_to_f16(e))) * g;
-    scale_byte = nan ? 0x7fu : (e & 0xffu);
+    scale_byte = amax != amax ? 0x7fu : (e & 0xffu);
     if (!(sg > 0.f)) return 0u;
     float y[8];
     if constexpr (EXACT) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) y[i] = __fdiv_rn(x[i], sg);
     } else {
-        const float r = __fdiv_rn(1.f, sg);
+        float r;
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(sg));
+        r *= UP;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] = __uint_as_float((__float_as_uint(x[i] * r) + 0x40u) & ~0x7fu);
+        for (int i = 0; i < 8; ++i) y[i] = cut16(x[i] * r);
     }
     uint32_t w;
     asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
@@ -126,6 +136,54 @@ template <class T, int N>
 struct alignas(sizeof(T) * N < 16 ? sizeof(T) * N : 16) Vec {
     T v[N];
 };
+
+// Pairs of elements: two from a 32-bit word (16-bit types), and back, rounding to nearest even.
+template <class T> struct Two;
+template <> struct Two<__nv_bfloat16> {
+    static __device__ __forceinline__ float2 get(const Vec<__nv_bfloat16, 2> &v) {
+        const uint32_t w = *reinterpret_cast<const uint32_t *>(&v);
+        return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+    }
+    static __device__ __forceinline__ void put(Vec<__nv_bfloat16, 2> &v, float a, float b) {
+        *reinterpret_cast<uint32_t *>(&v) = pack_bf16x2(a, b);
+    }
+};
+template <> struct Two<__half> {
+    static __device__ __forceinline__ float2 get(const Vec<__half, 2> &v) {
+        return __half22float2(*reinterpret_cast<const __half2 *>(&v));
+    }
+    static __device__ __forceinline__ void put(Vec<__half, 2> &v, float a, float b) {
+        *reinterpret_cast<uint32_t *>(&v) = q4::pack_f16x2(a, b);
+    }
+};
+template <> struct Two<float> {
+    static __device__ __forceinline__ float2 get(const Vec<float, 2> &v) { return make_float2(v.v[0], v.v[1]); }
+    static __device__ __forceinline__ void put(Vec<float, 2> &v, float a, float b) { v.v[0] = a; v.v[1] = b; }
+};
+template <class T, int V>
+__device__ __forceinline__ void widen(const Vec<T, V> &v, float (&x)[V]) {
+    if constexpr (V == 1) {
+        x[0] = to_f32(v.v[0]);
+    } else {
+#pragma unroll
+        for (int j = 0; j < V; j += 2) {
+            const float2 f = Two<T>::get(*reinterpret_cast<const Vec<T, 2> *>(&v.v[j]));
+            x[j] = f.x;
+            x[j + 1] = f.y;
+        }
+    }
+}
+template <class T, int V>
+__device__ __forceinline__ Vec<T, V> narrow(const float (&x)[V]) {
+    Vec<T, V> v;
+    if constexpr (V == 1) {
+        v.v[0] = from_f32<T>(x[0]);
+    } else {
+#pragma unroll
+        for (int j = 0; j < V; j += 2) Two<T>::put(*reinterpret_cast<Vec<T, 2> *>(&v.v[j]), x[j], x[j + 1]);
+    }
+    return v;
+}
 
 inline int dtype_size(int dtype) { return dtype == LSA_DTYPE_F32 ? 4 : 2; }
 inline bool dtype_known(int dtype) { return dtype >= LSA_DTYPE_BF16 && dtype <= LSA_DTYPE_F32; }

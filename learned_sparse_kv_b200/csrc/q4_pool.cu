@@ -18,18 +18,23 @@ struct Q4Side {
     uint8_t *pool;
     int64_t token_stride, head_stride;
     int W;
-    float g, g6;
+    float g, g6;         // g6: 6 g, or 1 / (6 g) for quantise_half without EXACT
 };
 
 // A thread's place: half group u of a token's rows (K's first, then V's).
 struct Place {
     const Q4Side &s;
     int h, col;          // head, first of the eight columns
-    __device__ Place(const Q4Side &a, const Q4Side &b, int u, int per_a) : s(u < per_a ? a : b) {
+    uint8_t *code, *scale;     // of slot 0, row 0
+    int64_t slot_bytes;
+    __device__ Place(const Q4Side &a, const Q4Side &b, int u, int per_a, int heads) : s(u < per_a ? a : b) {
         if (u >= per_a) u -= per_a;
         const int halves = s.W / 8;
         h = u / halves;
         col = (u - h * halves) * 8;
+        code = s.pool + h * q4::chunk_bytes(s.W) + col / 2;
+        scale = s.pool + h * q4::chunk_bytes(s.W) + q4::scale_base(s.W) + col / 16;
+        slot_bytes = heads * q4::chunk_bytes(s.W);
     }
 };
 
@@ -38,23 +43,23 @@ __device__ __forceinline__ void load8(const T *src, float (&x)[8]) {
     constexpr int PER = 16 / sizeof(T);
 #pragma unroll
     for (int i = 0; i < 8 / PER; ++i) {
-        const Vec<T, PER> v = *reinterpret_cast<const Vec<T, PER> *>(src + i * PER);
+        float f[PER];
+        widen(*reinterpret_cast<const Vec<T, PER> *>(src + i * PER), f);
 #pragma unroll
-        for (int j = 0; j < PER; ++j) x[i * PER + j] = to_f32(v.v[j]);
+        for (int j = 0; j < PER; ++j) x[i * PER + j] = f[j];
     }
 }
 
 // The whole warp calls; slot < 0: nothing is written.
 template <bool EXACT>
-__device__ __forceinline__ void put_half(const Place &at, int heads, int64_t slot, const float (&x)[8]) {
-    const Q4Side &s = at.s;
+__device__ __forceinline__ void put_half(const Place &at, int64_t slot, const float (&x)[8]) {
     uint32_t sb;
-    const uint32_t codes = q4::quantise_half<EXACT>(x, s.g, s.g6, sb);
+    const uint32_t codes = q4::quantise_half<EXACT>(x, at.s.g, at.s.g6, sb);
     if (slot < 0) return;
-    uint8_t *chunk = s.pool + ((slot / LSA_CHUNK) * heads + at.h) * q4::chunk_bytes(s.W);
-    const int r = (int)(slot % LSA_CHUNK);
-    *reinterpret_cast<uint32_t *>(chunk + r * q4::code_row(s.W) + at.col / 2) = codes;
-    if (!(at.col & 8)) chunk[q4::scale_base(s.W) + r * q4::scale_row(s.W) + at.col / 16] = (uint8_t)sb;
+    const int64_t chunk = (int64_t)((uint64_t)slot / LSA_CHUNK) * at.slot_bytes;
+    const int r = (int)((uint64_t)slot % LSA_CHUNK);
+    *reinterpret_cast<uint32_t *>(at.code + chunk + r * q4::code_row(at.s.W)) = codes;
+    if (!(at.col & 8)) at.scale[chunk + r * q4::scale_row(at.s.W)] = (uint8_t)sb;
 }
 
 // `per` half groups a token; where they are fewer than the block's threads, a block takes several tokens at once.
@@ -67,7 +72,7 @@ __global__ void __launch_bounds__(256) q4_write_kernel(const Q4Side a, const Q4S
     for (int u0 = 0; u0 < per; u0 += 256) {
         const int u = u0 + (int)threadIdx.x - mine * per;
         const bool live = mine < tokens && u < per;
-        const Place at(a, b, live ? u : 0, per_a);
+        const Place at(a, b, live ? u : 0, per_a, heads);
         const T *src = static_cast<const T *>(at.s.x) + at.h * at.s.head_stride + at.col;
         const int64_t step = (int64_t)gridDim.x * tokens;
         for (int64_t t0 = (int64_t)blockIdx.x * tokens; t0 < T_; t0 += 2 * step) {
@@ -87,9 +92,9 @@ __global__ void __launch_bounds__(256) q4_write_kernel(const Q4Side a, const Q4S
             }
 #pragma unroll
             for (int n = 0; n < 2; ++n) {
-                const bool there = slot[n] >= 0 && slot[n] < n_rows;
+                const bool there = (uint64_t)slot[n] < (uint64_t)n_rows;
                 if (!there && slot[n] != -1) flag(status, LSA_DEV_INDEX);
-                put_half<EXACT>(at, heads, there ? slot[n] : -1, x[n]);
+                put_half<EXACT>(at, there ? slot[n] : -1, x[n]);
             }
         }
     }
@@ -118,10 +123,10 @@ __global__ void __launch_bounds__(256) q4_append_kernel(const Q4Side a, const Q4
     for (int u0 = 0; u0 < per; u0 += 256) {
         const int u = u0 + (int)threadIdx.x;
         const bool live = u < per;
-        const Place at(a, b, live ? u : 0, per_a);
+        const Place at(a, b, live ? u : 0, per_a, heads);
         float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
         if (live) load8(static_cast<const T *>(at.s.x) + seq * at.s.token_stride + at.h * at.s.head_stride + at.col, x);
-        put_half<true>(at, heads, live ? row : -1, x);
+        put_half<true>(at, live ? row : -1, x);
     }
     if (li_pool)
         for (int c = threadIdx.x; c < dl / 8; c += 256)
@@ -138,48 +143,45 @@ __global__ void __launch_bounds__(256) q4_read_kernel(const uint8_t *__restrict_
     if (per < 256 && mine >= tokens) return;
     for (int u = per < 256 ? threadIdx.x - mine * per : threadIdx.x; u < per; u += 256) {
         const int h = u / halves, col = (u - h * halves) * 8;
-        const uint8_t *base = pool + h * q4::chunk_bytes(W);
-        const int64_t step = (int64_t)gridDim.x * tokens;
+        const uint8_t *code = pool + h * q4::chunk_bytes(W) + col / 2;
+        const uint8_t *scale = pool + h * q4::chunk_bytes(W) + q4::scale_base(W) + col / 16;
+        const int64_t slot_bytes = heads * q4::chunk_bytes(W), step = (int64_t)gridDim.x * tokens;
         for (int64_t t = (int64_t)blockIdx.x * tokens + (per < 256 ? mine : 0); t < T_; t += 4 * step) {
             // four tokens in flight
             int64_t slot[4];
             uint32_t codes[4], sb[4];
 #pragma unroll
-            for (int n = 0; n < 4; ++n) slot[n] = t + n * step < T_ ? slot_map[t + n * step] : -2;
+            for (int n = 0; n < 4; ++n) slot[n] = t + n * step < T_ ? slot_map[t + n * step] : -1;
 #pragma unroll
             for (int n = 0; n < 4; ++n) {
                 codes[n] = sb[n] = 0u;
-                if (slot[n] >= 0 && slot[n] < n_rows) {
-                    const uint8_t *chunk = base + (slot[n] / LSA_CHUNK) * heads * q4::chunk_bytes(W);
-                    const int r = (int)(slot[n] % LSA_CHUNK);
-                    codes[n] = *reinterpret_cast<const uint32_t *>(chunk + r * q4::code_row(W) + col / 2);
-                    sb[n] = chunk[q4::scale_base(W) + r * q4::scale_row(W) + col / 16];
+                if ((uint64_t)slot[n] < (uint64_t)n_rows) {
+                    const int64_t chunk = (int64_t)((uint64_t)slot[n] / LSA_CHUNK) * slot_bytes;
+                    const int r = (int)((uint64_t)slot[n] % LSA_CHUNK);
+                    codes[n] = *reinterpret_cast<const uint32_t *>(code + chunk + r * q4::code_row(W));
+                    sb[n] = scale[chunk + r * q4::scale_row(W)];
+                } else if (slot[n] != -1) {
+                    flag(status, LSA_DEV_INDEX);
                 }
             }
+            T *dst = out + (t * per + u) * 8;
 #pragma unroll
-            for (int n = 0; n < 4; ++n) {
+            for (int n = 0; n < 4; ++n, dst += step * per * 8) {
                 if (t + n * step >= T_) break;
-                if (slot[n] < -1 || slot[n] >= n_rows) flag(status, LSA_DEV_INDEX);
                 uint32_t p[4];
                 q4::e2m1x8_to_f16(codes[n], p);
                 const uint32_t s = q4::dup_lo(q4::e4m3x2_to_f16(sb[n]));
-                float x[8];
+                constexpr int PER = 16 / sizeof(T);
+                float x[8 / PER][PER];
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     const uint32_t v = q4::hmul2(p[k], s);     // exact: one rounding, with g
                     const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&v));
-                    x[2 * k] = f.x * g;
-                    x[2 * k + 1] = f.y * g;
+                    x[2 * k / PER][2 * k % PER] = f.x * g;
+                    x[2 * k / PER][2 * k % PER + 1] = f.y * g;
                 }
-                constexpr int PER = 16 / sizeof(T);
-                T *dst = out + ((t + n * step) * per + u) * 8;
 #pragma unroll
-                for (int k = 0; k < 8 / PER; ++k) {
-                    Vec<T, PER> v;
-#pragma unroll
-                    for (int j = 0; j < PER; ++j) v.v[j] = from_f32<T>(x[k * PER + j]);
-                    *reinterpret_cast<Vec<T, PER> *>(dst + k * PER) = v;
-                }
+                for (int k = 0; k < 8 / PER; ++k) *reinterpret_cast<Vec<T, PER> *>(dst + k * PER) = narrow<T, PER>(x[k]);
             }
         }
     }
@@ -241,6 +243,10 @@ extern "C" int lsa_write_q4(int dtype, int64_t T, int heads, const void *k, int6
     const int64_t rows = n_slots * LSA_CHUNK;
     // 16-bit rows and power-of-two scales need no division (quantise_half): 16384 tokens, 8 heads, K and V
     const bool exact = dtype == LSA_DTYPE_F32 || !power_of_two(k_scale) || (two && !power_of_two(v_scale));
+    if (!exact) {
+        a.g6 = 1.f / a.g6;
+        if (two) b.g6 = 1.f / b.g6;
+    }
     const int blocks = q4_blocks(T, per, 2);
 #define LSA_WRITE(TYPE, E) q4_write_kernel<TYPE, E><<<blocks, 256, 0, stream>>>(a, b, heads, T, per, per_a, rows, slot_map, dev_status)
     if (dtype == LSA_DTYPE_F32) LSA_WRITE(float, true);
