@@ -98,8 +98,8 @@ __global__ void __launch_bounds__(THREADS, ITEMS == 1 ? 5 : 1) norm_rope_kernel(
         col[i] = item < pairs ? p.ro + item * V : (INTER || rest < p.ro ? rest : rest + p.rd);
         turn[i] = have[i] && (INTER ? col[i] >= p.ro && col[i] < p.ro + p.rd : item < pairs);
     }
-    // The groups of a warp take the same turns, so that the shuffles need no masks of their own (shuffles under
-    // masks that differ from lane to lane are serialised: 36 us instead of SHFL_US for 8192 tokens of 40 rows).
+    // The groups of a warp take the same turns, so that the shuffles need no masks of their own: shuffles under
+    // masks that differ from lane to lane are serialised.
     const int first = blockIdx.y * p.per_token, step = gridDim.y * p.per_token;
     Vec<T, V> xa[ITEMS], xb[IB];
     auto fetch = [&](const Side &s, int h) {

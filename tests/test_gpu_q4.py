@@ -108,6 +108,45 @@ def test_write_special_values_and_strides(L):
     np.testing.assert_array_equal(got, ref)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("g", [1.0, 2.0 ** -5, 0.75])
+def test_write_every_significand(L, dtype, g):
+    """Every value of the type over five octaves below the group's maximum, for each significand of the
+    scale, halfway cases among them; and every significand of the maximum itself."""
+    bits = np.arange(1 << 16, dtype=np.uint16).view(np.int16)
+    every = torch.from_numpy(bits).view(dtype).double()
+    groups = []
+    for m in range(8):
+        s = (1 + m / 8) * g
+        top = 6.0 * s
+        x = every[(every.abs() <= top) & (every.abs() >= top / 32)]
+        x = torch.cat([x, torch.zeros(-len(x) % 15, dtype=torch.float64)]).view(-1, 15)
+        groups.append(torch.cat([x, torch.full((len(x), 1), top, dtype=torch.float64)], 1))
+    x = every[(every >= 1) & (every < 8)]
+    groups.append(torch.cat([x[:, None], torch.zeros(len(x), 15, dtype=torch.float64)], 1))
+    x = torch.cat(groups).to(dtype)
+    x = torch.cat([x, torch.zeros(-len(x) % 4, 16, dtype=dtype)]).view(-1, 1, 64)
+    T = len(x)
+    pool = L.q4_pool(T // CH + 1, 1, 64)
+    L.write_q4(x.cuda(), pool, torch.arange(T, device="cuda"), k_scale=g)
+    codes, scales = R.unpack(pool.cpu().numpy())
+    # g = 0.75: the product s g and the quotients are rounded to fp32 before the codes, as the definition has it
+    qc, qs = R.quantise(x.double().numpy(), g) if g != 0.75 else _fp32_quantise(x.float().numpy(), np.float32(g))
+    np.testing.assert_array_equal(scales.transpose(0, 2, 1, 3).reshape(-1, 1, 4)[:T], qs)
+    np.testing.assert_array_equal(codes.transpose(0, 2, 1, 3).reshape(-1, 1, 64)[:T], qc)
+
+
+def _fp32_quantise(x, g):
+    """R.quantise with its two quotients and one product rounded to fp32."""
+    grp = x.reshape(x.shape[:-1] + (-1, 16))
+    t = np.minimum(np.abs(grp).max(-1) / (np.float32(6) * g), np.float32(448))
+    sb = R._nearest_even(t.astype(np.float64), R.E4M3)
+    sg = (R.E4M3[sb].astype(np.float32) * g)[..., None]
+    y = np.divide(np.abs(grp), sg, out=np.zeros_like(grp), where=sg > 0)
+    code = R._nearest_even(y.astype(np.float64), R.E2M1) + 8 * (np.signbit(grp) & (sg > 0))
+    return code.reshape(x.shape).astype(np.uint8), sb.astype(np.uint8)
+
+
 def test_write_skips_and_flags_slots_outside_the_pool(L):
     x = torch.ones(3, 1, 64, device="cuda")
     pool = L.q4_pool(2, 1, 64)

@@ -52,7 +52,8 @@ def _table(rng, cached, stride, n_slots):
 
 @pytest.mark.parametrize("B,stride,hi_cached,hi_new,n_slots", [
     (1, 1, 1, 63, 1), (1, 5, 300, 20, 7), (3, 9, 250, 200, 40), (32, 65, 4000, 1, 2100), (300, 17, 900, 100, 5200),
-    (1500, 4, 120, 60, 4600), (7, 2000, 120000, 500, 15001), (2, 40, 1, 2400, 100001)])
+    (1500, 4, 120, 60, 4600), (7, 2000, 120000, 500, 15001), (2, 40, 1, 2400, 100001),
+    (5000, 3, 60, 60, 11000), (300, 7100, 2000, 40, 9900)])      # the last two: more than one cluster takes
 def test_tables_exact(L, B, stride, hi_cached, hi_new, n_slots):
     rng = np.random.default_rng(B + stride)
     cached = rng.integers(0, hi_cached + 1, B)
