@@ -20,8 +20,8 @@
 // TMEM per CTA: two S buffers of 64 columns and O = 64 heads x 512 values in 256 columns.
 // Warp roles:
 //   0      MMA issuer (even CTA)            2   TMEM allocator
-//   4..7   softmax, O rescale, epilogue (one thread per TMEM lane: head x unit of the tile)
-//   8..15  dequantise K                    16..23  dequantise V, row masks
+//   4..7   softmax, O rescale (one thread per TMEM lane: head x unit of the tile)
+//   8..15  dequantise K                    16..23  dequantise V, row masks; both write O at the end
 // (Eight warps each: with four the conversion, a chain of dependent instructions, took 3000
 // cycles a tile and paced the pipeline while the issue slots were 25 % used.)
 // Every mbarrier wait is bounded: on timeout the kernel sets LSA_DEV_TIMEOUT and the abort flag of
@@ -60,6 +60,7 @@ struct __align__(1024) Smem {
     uint64_t pv_full[2];                // the even CTA's, 16 arrivals: V and P of unit a of the tile are written
     uint64_t pv_done[2];                // P V over unit a is done: its V and P may be rewritten
     uint64_t s_full[2];                 // S buffers
+    uint64_t s_last;                    // Q K^T of the last tile is done
     uint64_t info_full[INFO];
     uint64_t mma_done;
     uint64_t never;                     // no arrival ever: the failure-path test's wait
@@ -206,6 +207,7 @@ __global__ void __launch_bounds__(THREADS, 1) q4_mla_kernel(const DecodeParams p
             mbar_init(&sm.s_full[i], 1);
         }
         for (int i = 0; i < INFO; ++i) mbar_init(&sm.info_full[i], DEQ);
+        mbar_init(&sm.s_last, 1);
         mbar_init(&sm.mma_done, 1);
         mbar_init(&sm.never, 1);
         sm.abort_flag = 0;
@@ -259,18 +261,24 @@ __global__ void __launch_bounds__(THREADS, 1) q4_mla_kernel(const DecodeParams p
         slot1 = row_slot(p, b, pos1);
         row0 = pool_row(p, pos0, slot0);
         load(row0);
-    }
-    if (n_tiles > 0) {
-        // ---- queries as f16 over a power of two, straight into the operand layout
+    } else if (n_tiles > 0) {
+        // ---- warps 0..7: queries as f16 over a power of two, straight into the operand layout, four heads at a time
         const uint32_t qb = smem_addr(sm.q);
 #pragma unroll 1
-        for (int h = warp; h < HPC; h += THREADS / 32) {
-            const int head = HPC * (int)rank + h;
+        for (int h0 = 8 * warp; h0 < 8 * warp + 8; h0 += 4) {
+        uint4 held[4][3];
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+            const int head = HPC * (int)rank + h0 + n;
             const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.q) + ((size_t)b * p.Hq + head) * DQK);
-            uint4 raw[3];
 #pragma unroll
             for (int i = 0; i < 3; ++i)
-                raw[i] = head < p.Hq && lane + 32 * i < DQK / 8 ? __ldg(src + lane + 32 * i) : make_uint4(0, 0, 0, 0);
+                held[n][i] = head < p.Hq && lane + 32 * i < DQK / 8 ? __ldg(src + lane + 32 * i) : make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+            const int h = h0 + n;
+            const uint4 (&raw)[3] = held[n];
             float x[3][8];
             float amax = 0.f;
 #pragma unroll
@@ -302,6 +310,7 @@ __global__ void __launch_bounds__(THREADS, 1) q4_mla_kernel(const DecodeParams p
                                  "r"(q4::pack_f16x2(x[i][4] * inv, x[i][5] * inv)), "r"(q4::pack_f16x2(x[i][6] * inv, x[i][7] * inv))
                                  : "memory");
             }
+        }
         }
         fence_proxy_async_smem();
     }
@@ -341,6 +350,7 @@ __global__ void __launch_bounds__(THREADS, 1) q4_mla_kernel(const DecodeParams p
                         umma_commit_pair(&sm.k_empty[g], 0x3);
                     }
                     umma_commit_pair(&sm.s_full[sb], 0x3);
+                    if (n == n_tiles - 1) umma_commit_pair(&sm.s_last, 0x3);
                 }
                 __syncwarp();
             }
@@ -540,12 +550,28 @@ __global__ void __launch_bounds__(THREADS, 1) q4_mla_kernel(const DecodeParams p
             p.m_part[part0 + head] = m_ref - q4::P_SHIFT;
             p.l_part[part0 + head] = l_tot;
         }
-        // O leaves tensor memory 32 columns at a time and passes through shared memory (the P
-        // buffers), so that every store instruction writes whole 128-byte row pieces.
-        float *xbuf = reinterpret_cast<float *>(sm.p[0]) + (warp & 3) * 1024;
-        const int head0 = HPC * (int)rank + (32 * (warp & 3) & 63);
+    }
+
+    // ---- epilogue of O, by the 16 warps that dequantised (four column blocks at a time)
+    if (warp >= 8) {
+        // A parity tells the last two phases apart, no more, so the last P V is waited for in step: Q K^T of the last
+        // tile comes after P V of tile n - 3, then tiles n - 2 and n - 1 in turn.
+        bool ok = n_tiles == 0 || warp_wait(sm, &sm.s_last, 0, p.status);
 #pragma unroll 1
-        for (int q = 0; q < 8; ++q) {
+        for (int i = 0; i < 4 && n_tiles > 0 && ok; ++i) {
+            const int u = n_tiles - 2 + (i >> 1);
+            if (u >= 0) ok = warp_wait(sm, &sm.pv_done[i & 1], u & 1, p.status);
+        }
+        tc_fence_after();
+        // O leaves tensor memory 32 columns at a time and passes through shared memory (the K buffer, free now),
+        // so that every store instruction writes whole 128-byte row pieces.
+        float *xbuf = reinterpret_cast<float *>(sm.k) + (warp - 8) * 1024;
+        const uint32_t lane_base = (uint32_t)(32 * (warp & 3)) << 16;
+        const int half = (warp & 3) >> 1;                      // lanes 64..127 hold the second half of the columns
+        const int head0 = HPC * (int)rank + (32 * (warp & 3) & 63);
+        const size_t part0 = ((size_t)b * p.n_splits + split) * p.Hq;
+#pragma unroll 1
+        for (int q = (warp - 8) >> 2; q < 8; q += 4) {
             uint32_t o[32];
             if (n_tiles > 0) {
                 tmem_ld32(tmem + lane_base + TM_O + 32 * q, o);
