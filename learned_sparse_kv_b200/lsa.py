@@ -1,4 +1,4 @@
-"""ctypes binding of liblsa.so: argument marshalling only.
+"""Binding of liblsa.so: argument marshalling only (ctypes, and csrc/binding.cpp for the shortest calls).
 
 Every step of the decode path runs in the library's CUDA kernels.  Tensors are
 torch tensors (bf16 inputs as torch.bfloat16); the binding allocates outputs
@@ -7,7 +7,8 @@ and turns a non-zero status into an LSAError.  There is no CPU fallback: if
 the library is missing the import fails.
 """
 import ctypes
-import functools
+import importlib.machinery
+import importlib.util
 import os
 
 import torch
@@ -437,92 +438,40 @@ def advance_window(window_start, window_len, by, new_len, *, stream=None):
 
 # ------------------------------------------- tables, norm + rotation ----
 #
-# These calls are short on the device, so the host side is kept short too: one check per tensor
-# (_arg), pointers as plain integers, no device switch unless the tensors are on another device.
+# These calls are short on the device, so their checks, allocations and marshalling are native too
+# (csrc/binding.cpp); the functions here are their signatures.
 
-DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
-_I32, _I64, _U8, _F32, _BF16 = torch.int32, torch.int64, torch.uint8, torch.float32, torch.bfloat16
-
-
-def _dtype(dt, name):
-    code = DTYPES.get(dt)
-    if code is None:
-        raise LSAError(1, f"{name} must be bfloat16, float16 or float32, got {dt}")
-    return code
-
-
-def _cuda(t, dims, name):
-    """Device index of a CUDA tensor of one of the given dimension counts."""
-    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dim() in dims):
-        raise LSAError(1, f"{name} must be a CUDA tensor of {' or '.join(map(str, dims))} dimensions")
-    return t.get_device()
+def _load_binding():
+    path = os.path.join(_HERE, "_binding.so")
+    if not os.path.exists(path):
+        raise ImportError(f"_binding.so not found at {path}; build it with `python -m learned_sparse_kv_b200.build`")
+    spec = importlib.util.spec_from_file_location("_binding", path,
+                                                  loader=importlib.machinery.ExtensionFileLoader("_binding", path))
+    module = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(module)
+    module.set_error_type(LSAError)
+    return module
 
 
-def _arg(t, dtype, shape, index, name):
-    """Address of a contiguous tensor of that type, shape and device."""
-    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == index \
-            and t.is_contiguous():
-        return t.data_ptr()
-    if not (isinstance(t, torch.Tensor) and t.is_cuda):
-        raise LSAError(1, f"{name} must be a CUDA tensor")
-    if t.dtype is not dtype:
-        raise LSAError(1, f"{name} must be {dtype}, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
-        raise LSAError(1, f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.get_device() != index:
-        raise LSAError(1, f"{name} must be on cuda:{index}, like the first argument")
-    raise LSAError(1, f"{name} must be contiguous")
+_native = _load_binding()
 
 
-def _status(t, index):
-    if t is None:
-        return None
-    if t.dtype is _I32 and t.is_cuda and t.get_device() == index and t.numel() >= 1:
-        return t.data_ptr()
-    raise LSAError(1, f"status must be an int32 tensor on cuda:{index}")
-
-
-class _NoSwitch:
-    def __enter__(self):
-        pass
-
-    def __exit__(self, *exc):
-        return False
-
-
-_NO_SWITCH = _NoSwitch()
-
-
-# torch's own short cut to the current stream's handle (no Stream object), where this torch has it
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
-    (lambda index: torch.cuda.current_stream(index).cuda_stream)
-
-
-def _on(index):
-    """Makes device `index` current for the call, if it is not."""
-    return _NO_SWITCH if torch.cuda.current_device() == index else torch.cuda.device(index)
-
-
-def _handle(index, stream):
-    return _raw_stream(index) if stream is None else stream.cuda_stream
-
-
-def _workspace(nbytes, ws, dev, index):
-    if ws is None:
-        return torch.empty(nbytes if nbytes > 256 else 256, dtype=_U8, device=dev)
-    if not (ws.dtype is _U8 and ws.is_cuda and ws.get_device() == index and ws.is_contiguous()):
-        raise LSAError(1, f"ws must be a contiguous uint8 tensor on cuda:{index}")
+def _side_workspace(nbytes, first, stream):
+    """A workspace for work on a side stream: it stays reserved until that work is done."""
+    ws = torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device=getattr(first, "device", "cuda"))
+    if ws.is_cuda:
+        ws.record_stream(stream)
     return ws
 
 
-def _side(stream, index, *fresh):
-    """Tensors made here on the current stream stay reserved until the work on `stream` is done."""
-    if stream is not None and stream != torch.cuda.current_stream(index):
-        for t in fresh:
+def _on_side(stream, outputs):
+    """Outputs made on the current stream and written on `stream`."""
+    for t in outputs:
+        if t is not None:
             t.record_stream(stream)
+    return outputs
 
 
-@functools.lru_cache(maxsize=256)
 def build_tables_workspace_size(B, table_stride, n_slots):
     return _lib.lsa_build_tables_workspace_size(B, table_stride, n_slots)
 
@@ -535,59 +484,13 @@ def build_tables(table, cached_len, new_len, n_slots, max_new, *, table_next=Non
     slot_map [max_new] int64, position [max_new] int32, new_offset [B + 1] int32, n_free [1] int32); map entries behind
     the last new token are -1.
     """
-    index = _cuda(table, (2,), "table")
-    B, stride = table.shape
-    dev = table.device
-    if max_new < 0:
-        raise LSAError(1, "max_new must not be negative")
-    with _on(index):
-        if table_next is None:
-            table_next = torch.empty_like(table)
-        if slot_map is None:
-            slot_map = torch.empty(max_new, dtype=_I64, device=dev)
-        if position is None and new_offset is None and n_free is None:     # one allocation
-            position, new_offset, n_free = torch.empty(max_new + B + 2, dtype=_I32, device=dev).split((max_new, B + 1, 1))
-        if position is None:
-            position = torch.empty(max_new, dtype=_I32, device=dev)
-        if new_offset is None:
-            new_offset = torch.empty(B + 1, dtype=_I32, device=dev)
-        if n_free is None:
-            n_free = torch.empty(1, dtype=_I32, device=dev)
-        ws = _workspace(build_tables_workspace_size(B, stride, n_slots), ws, dev, index)
-        _check(_lib.lsa_build_tables(
-            _arg(table, _I32, (B, stride), index, "table"), stride, _arg(cached_len, _I32, (B,), index, "cached_len"),
-            _arg(new_len, _I32, (B,), index, "new_len"), B, n_slots, max_new,
-            _arg(table_next, _I32, (B, stride), index, "table_next"), _arg(slot_map, _I64, (max_new,), index, "slot_map"),
-            _arg(position, _I32, (max_new,), index, "position"), _arg(new_offset, _I32, (B + 1,), index, "new_offset"),
-            _arg(n_free, _I32, (1,), index, "n_free"), _status(status, index), ws.data_ptr(), ws.numel(),
-            _handle(index, stream)))
-        if stream is not None:
-            _side(stream, index, ws, table_next, slot_map, position, new_offset, n_free)
-    return table_next, slot_map, position, new_offset, n_free
-
-
-def _rows(t, name, dtype, T, heads, D, index):
-    """Address, token stride and head stride of rows [T, heads, D] with contiguous columns."""
-    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == (T, heads, D) and t.get_device() == index):
-        if not (isinstance(t, torch.Tensor) and t.is_cuda):
-            raise LSAError(1, f"{name} must be a CUDA tensor")
-        if t.dtype is not dtype:
-            raise LSAError(1, f"{name} must be {dtype}, got {t.dtype}")
-        if t.get_device() != index:
-            raise LSAError(1, f"{name} must be on cuda:{index}, like the first argument")
-        raise LSAError(1, f"{name} must be [{T}, {heads}, {D}], got {tuple(t.shape)}")
-    st, sh, sc = t.stride()
-    if sc != 1 and D > 1 and T * heads > 0:
-        raise LSAError(1, f"{name} must have contiguous columns")
-    # the stride of a dimension of one row is never used; torch may report anything for it
-    return t.data_ptr(), st if T > 1 else 0, sh if heads > 1 else 0
-
-
-def _norm(w, width, dtype, index, name):
-    if w is None:
-        return None, 0 if width is None else int(width)
-    n = w.numel() if width is None else int(width)
-    return (_arg(w, dtype, (n,), index, name) if n > 0 else None), n
+    if stream is None:
+        return _native.build_tables(table, cached_len, new_len, n_slots, max_new, table_next, slot_map, position,
+                                    new_offset, n_free, status, ws, None)
+    if ws is None:
+        ws = _side_workspace(build_tables_workspace_size(*table.shape, n_slots), table, stream)
+    return _on_side(stream, _native.build_tables(table, cached_len, new_len, n_slots, max_new, table_next, slot_map,
+                                                 position, new_offset, n_free, status, ws, stream.cuda_stream))
 
 
 def qk_norm_rope(q, k, position, inv_freq, *, q_weight=None, k_weight=None, q_norm_width=None, k_norm_width=None,
@@ -599,34 +502,11 @@ def qk_norm_rope(q, k, position, inv_freq, *, q_weight=None, k_weight=None, q_no
     k_norm_width columns (default: the weight's length, or none without a weight); the rotation covers columns
     [rot_offset, rot_offset + rot_dim).  Returns (q_out, k_out); outputs may be the inputs.
     """
-    index = _cuda(q, (3,), "q")
-    T, Hq, D = q.shape
-    dt = q.dtype
-    code = _dtype(dt, "q")
-    if not (isinstance(inv_freq, torch.Tensor) and inv_freq.dim() == 1):
-        raise LSAError(1, "inv_freq must have one dimension")
-    half = inv_freq.shape[0]
-    qw, qn = _norm(q_weight, q_norm_width, dt, index, "q_weight")
-    kw, kn = _norm(k_weight, k_norm_width, dt, index, "k_weight")
-    with _on(index):
-        if q_out is None:
-            q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
-        kp = ko = (None, 0, 0)
-        Hk = 0
-        if k is not None:
-            _cuda(k, (3,), "k")
-            Hk = k.shape[1]
-            if k_out is None:
-                k_out = torch.empty_like(k, memory_format=torch.contiguous_format)
-            kp, ko = _rows(k, "k", dt, T, Hk, D, index), _rows(k_out, "k_out", dt, T, Hk, D, index)
-        _check(_lib.lsa_qk_norm_rope(
-            code, T, D, *_rows(q, "q", dt, T, Hq, D, index), Hq, qw, qn, *_rows(q_out, "q_out", dt, T, Hq, D, index), *kp,
-            Hk, kw, kn, *ko, eps, _arg(position, _I32, (T,), index, "position"),
-            _arg(inv_freq, _F32, (half,), index, "inv_freq"), rot_offset, 2 * half, 1 if interleaved else 0,
-            _handle(index, stream)))
-        if stream is not None:
-            _side(stream, index, q_out, *([] if k is None else [k_out]))
-    return q_out, k_out
+    if stream is None:
+        return _native.qk_norm_rope(q, k, position, inv_freq, q_weight, k_weight, q_norm_width, k_norm_width, eps,
+                                    rot_offset, interleaved, q_out, k_out, None)
+    return _on_side(stream, _native.qk_norm_rope(q, k, position, inv_freq, q_weight, k_weight, q_norm_width, k_norm_width,
+                                                 eps, rot_offset, interleaved, q_out, k_out, stream.cuda_stream))
 
 
 # ------------------------------------------------------- 4-bit pools ----
@@ -644,95 +524,27 @@ def q4_pool(n_slots, heads, width, device="cuda"):
     return torch.zeros(n_slots, heads, q4_chunk_bytes(width), dtype=torch.uint8, device=device)
 
 
-def _pool_shape(t, name):
-    """(slots, heads, width) of a 4-bit pool."""
-    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dim() == 3 and t.shape[2] % 576 == 0 and t.shape[2] > 0):
-        raise LSAError(1, f"{name} must be a 4-bit pool on a CUDA device, [n_slots, heads, 36 * width] uint8")
-    n, heads, nb = t.shape
-    return n, heads, nb // 36
-
-
-def _q4_rows(x, name):
-    """[T, width] rows are one head."""
-    if _cuda(x, (2, 3), name) >= 0 and x.dim() == 2:
-        return x.unsqueeze(1)
-    return x
-
-
 def write_q4(k, k_pool, slot_map, *, v=None, v_pool=None, k_scale=1.0, v_scale=1.0, status=None, stream=None):
-    """Quantises rows k [T, heads, width] (and v) into 4-bit pools at slot_map [T] int64 (slot * 64 + row, -1: skip)."""
-    k = _q4_rows(k, "k")
-    index, dt = k.get_device(), k.dtype
-    T, heads, kw = k.shape
-    code = _dtype(dt, "k")
-    n_slots = _pool_shape(k_pool, "k_pool")[0]
-    if (v is None) != (v_pool is None):
-        raise LSAError(1, "v and v_pool come together")
-    vp, vw, vpool = (None, 0, 0), 0, None
-    if v is not None:
-        v = _q4_rows(v, "v")
-        vw = v.shape[2]
-        vp = _rows(v, "v", dt, T, heads, vw, index)
-        vpool = _arg(v_pool, _U8, (n_slots, heads, 36 * vw), index, "v_pool")
-    with _on(index):
-        _check(_lib.lsa_write_q4(
-            code, T, heads, *_rows(k, "k", dt, T, heads, kw, index), kw,
-            _arg(k_pool, _U8, (n_slots, heads, 36 * kw), index, "k_pool"), k_scale, *vp, vw, vpool, v_scale, n_slots,
-            _arg(slot_map, _I64, (T,), index, "slot_map"), _status(status, index), _handle(index, stream)))
+    """Quantises rows k [T, heads, width] (or [T, width]) and v into 4-bit pools at slot_map [T] int64 (slot * 64 + row,
+    -1: skip)."""
+    _native.write_q4(k, k_pool, slot_map, v, v_pool, k_scale, v_scale, status,
+                     None if stream is None else stream.cuda_stream)
 
 
 def append_token_q4(new_k, new_v, new_li, k_pool, v_pool, li_pool, chunk_table, window_start, window_len, *,
                     k_scale=1.0, v_scale=1.0, status=None, stream=None):
     """append_token for 4-bit pools: new_k [B, heads, width] (or [B, width]), new_v likewise or None (latent)."""
-    new_k = _q4_rows(new_k, "new_k")
-    index, dt = new_k.get_device(), new_k.dtype
-    B, heads, kw = new_k.shape
-    code = _dtype(dt, "new_k")
-    n_slots = _pool_shape(k_pool, "k_pool")[0]
-    if (new_v is None) != (v_pool is None):
-        raise LSAError(1, "new_v and v_pool come together")
-    vw = dl = 0
-    vp = vpool = li = lip = None
-    if new_v is not None:
-        new_v = _q4_rows(new_v, "new_v")
-        vw = new_v.shape[2]
-        vp = _arg(new_v, dt, (B, heads, vw), index, "new_v")
-        vpool = _arg(v_pool, _U8, (n_slots, heads, 36 * vw), index, "v_pool")
-    if new_li is not None or li_pool is not None:
-        _cuda(li_pool, (3,), "li_pool")
-        dl = li_pool.shape[2]
-        li, lip = _arg(new_li, _BF16, (B, dl), index, "new_li"), _arg(li_pool, _BF16, (n_slots, CHUNK, dl), index, "li_pool")
-    _cuda(chunk_table, (2,), "chunk_table")
-    stride = chunk_table.shape[1]
-    with _on(index):
-        _check(_lib.lsa_append_token_q4(
-            code, heads, _arg(new_k, dt, (B, heads, kw), index, "new_k"), kw,
-            _arg(k_pool, _U8, (n_slots, heads, 36 * kw), index, "k_pool"), k_scale, vp, vw, vpool, v_scale, li, lip, dl,
-            n_slots, _arg(chunk_table, _I32, (B, stride), index, "chunk_table"), stride,
-            _arg(window_start, _I32, (B,), index, "window_start"), _arg(window_len, _I32, (B,), index, "window_len"), B,
-            _status(status, index), _handle(index, stream)))
+    _native.append_token_q4(new_k, new_v, new_li, k_pool, v_pool, li_pool, chunk_table, window_start, window_len, k_scale,
+                            v_scale, status, None if stream is None else stream.cuda_stream)
 
 
 def read_q4(pool, slot_map, *, scale=1.0, out=None, out_dtype=torch.bfloat16, status=None, stream=None):
     """Rows slot_map [T] of a 4-bit pool as values [T, heads, width] (zeros where slot_map is -1)."""
-    n_slots, heads, width = _pool_shape(pool, "pool")
-    index = pool.get_device()
-    _cuda(slot_map, (1,), "slot_map")
-    T = slot_map.shape[0]
-    with _on(index):
-        if out is None:
-            _dtype(out_dtype, "out")
-            out = torch.empty(T, heads, width, dtype=out_dtype, device=pool.device)
-        _check(_lib.lsa_read_q4(
-            _arg(pool, _U8, (n_slots, heads, 36 * width), index, "pool"), n_slots, heads, width, scale,
-            _arg(slot_map, _I64, (T,), index, "slot_map"), T, _dtype(out.dtype, "out"),
-            _arg(out, out.dtype, (T, heads, width), index, "out"), _status(status, index), _handle(index, stream)))
-        if stream is not None:
-            _side(stream, index, out)
-    return out
+    if stream is None:
+        return _native.read_q4(pool, slot_map, scale, out, out_dtype, status, None)
+    return _on_side(stream, (_native.read_q4(pool, slot_map, scale, out, out_dtype, status, stream.cuda_stream),))[0]
 
 
-@functools.lru_cache(maxsize=256)
 def sparse_decode_q4_workspace_size(B, Hq, heads, dqk, dv, k, max_window_len):
     return _lib.lsa_sparse_decode_q4_workspace_size(B, Hq, heads, dqk, dv, k, max_window_len)
 
@@ -745,38 +557,17 @@ def sparse_decode_q4(q, k_pool, v_pool, chunk_table, topk_idx, topk_count, windo
 
     Returns (out [B, Hq, dv] of out_dtype, lse [B, Hq] fp32 or None).
     """
-    index = _cuda(q, (3,), "q")
-    B, Hq, dqk = q.shape
-    dev = q.device
-    n_slots, heads, _ = _pool_shape(k_pool, "k_pool")
-    vpool = None if v_pool is None else _arg(v_pool, _U8, (n_slots, heads, 36 * dv), index, "v_pool")
-    k, ti, tc = 0, None, None
-    if topk_idx is not None:
-        _cuda(topk_idx, (2,), "topk_idx")
-        k = topk_idx.shape[1]
-        if k:
-            ti, tc = _arg(topk_idx, _I32, (B, k), index, "topk_idx"), _arg(topk_count, _I32, (B,), index, "topk_count")
-    _cuda(chunk_table, (2,), "chunk_table")
-    stride = chunk_table.shape[1]
-    with _on(index):
-        if out is None:
-            _dtype(out_dtype, "out")
-            out = torch.empty(B, Hq, dv, dtype=out_dtype, device=dev)
-        if lse is None and want_lse:
-            lse = torch.empty(B, Hq, dtype=_F32, device=dev)
-        ws = _workspace(sparse_decode_q4_workspace_size(B, Hq, heads, dqk, dv, k, max_window_len), ws, dev, index)
-        _check(_lib.lsa_sparse_decode_q4(
-            _dtype(q.dtype, "q"), _arg(q, q.dtype, (B, Hq, dqk), index, "q"),
-            _arg(k_pool, _U8, (n_slots, heads, 36 * dqk), index, "k_pool"), k_scale, vpool, v_scale, n_slots, heads,
-            _arg(chunk_table, _I32, (B, stride), index, "chunk_table"), stride, ti, tc, k,
-            _arg(window_start, _I32, (B,), index, "window_start"), _arg(window_len, _I32, (B,), index, "window_len"),
-            max_window_len, B, Hq, dqk, dv, scale, _dtype(out.dtype, "out"),
-            _arg(out, out.dtype, (B, Hq, dv), index, "out"),
-            None if lse is None else _arg(lse, _F32, (B, Hq), index, "lse"), _status(status, index), ws.data_ptr(),
-            ws.numel(), _handle(index, stream)))
-        if stream is not None:
-            _side(stream, index, ws, out, *([] if lse is None else [lse]))
-    return out, lse
+    if stream is None:
+        return _native.sparse_decode_q4(q, k_pool, v_pool, chunk_table, topk_idx, topk_count, window_start, window_len,
+                                        max_window_len, dv, scale, k_scale, v_scale, out, out_dtype, lse, want_lse, status,
+                                        ws, None)
+    if ws is None:
+        B, Hq, dqk = q.shape
+        k = 0 if topk_idx is None else topk_idx.shape[-1]
+        ws = _side_workspace(sparse_decode_q4_workspace_size(B, Hq, k_pool.shape[1], dqk, dv, k, max_window_len), q, stream)
+    return _on_side(stream, _native.sparse_decode_q4(q, k_pool, v_pool, chunk_table, topk_idx, topk_count, window_start,
+                                                     window_len, max_window_len, dv, scale, k_scale, v_scale, out,
+                                                     out_dtype, lse, want_lse, status, ws, stream.cuda_stream))
 
 
 # ------------------------------------------------------------------- a7 ----
