@@ -8,12 +8,12 @@
 // Token i of request b sits at position cached + i, in pool row slot * 64 + position % 64.
 //
 // The work is small (4 bytes a table entry); dependent lookups and launches are what it costs.  Up to 2M table
-// entries and 4096 requests one cluster of 16 CTAs does everything in one launch, its phases
-// separated by cluster barriers: clear the bitmap of used slots | mark the kept ones | count the free
-// ones | list as many as are needed | write tables and maps.  Larger problems use all
-// multiprocessors: five launches (clear, mark, scan by one CTA, tables, maps).  32 requests of 16K to
-// 512K tokens (1 MB of tables, 73K kept chunks): 16.2 us on the device in one launch, of which the marks, one
-// atomic a chunk, take 6; 14.5 us in five launches, whose calls take the host 39 us instead of 23.
+// entries and 2048 requests one cluster of 16 CTAs does everything in one launch, its phases
+// separated by cluster barriers: clear the bitmap of used slots | mark the kept ones and copy their
+// entries | count the free ones | give as many as are needed to the new chunks | write the maps.
+// Larger problems use all multiprocessors: five launches (clear, mark, scan by one CTA, tables,
+// maps).  32 requests of 16K to 512K tokens (1 MB of tables, 73K kept chunks): 14.5 us on the device either
+// way, of which the marks, one atomic a chunk, take 5; the call takes 14.5 instead of 39.
 #include <limits.h>
 
 #include "block_scan.cuh"
@@ -160,7 +160,7 @@ __global__ void __launch_bounds__(256) map_kernel(const Params p) {
 
 // ---- one cluster
 
-constexpr int CL = 16, CL_THREADS = 1024, CL_REQUESTS = 4096, CL_ENTRIES = 1 << 21;
+constexpr int CL = 16, CL_THREADS = 1024, CL_REQUESTS = 2048, CL_ENTRIES = 1 << 21;
 constexpr int ROW = 256;       // table entries of one warp's turn
 
 __device__ __forceinline__ void cluster_barrier() {
@@ -176,8 +176,9 @@ __device__ __forceinline__ uint32_t load_l2(const uint32_t *p) { return __ldcg(p
 
 __global__ void __launch_bounds__(CL_THREADS, 1) cluster_kernel(const Params p) {
     __shared__ int warp_tot[CL_THREADS / 32 + 1];
-    __shared__ int base[CL_REQUESTS + 1], first_token[CL_REQUESTS + 1];   // of each request: new chunks, new tokens before it
     __shared__ int free_of[CL];
+    // of each request: new chunks and new tokens before it, chunks it keeps, tokens it has
+    __shared__ int base[CL_REQUESTS + 1], first_token[CL_REQUESTS + 1], have[CL_REQUESTS], cached[CL_REQUESTS];
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
     const int rank = (int)cta_of_cluster(), gt = rank * CL_THREADS + t;
     constexpr int ALL = CL * CL_THREADS, WARPS = ALL / 32;
@@ -195,6 +196,8 @@ __global__ void __launch_bounds__(CL_THREADS, 1) cluster_kernel(const Params p) 
             const Lengths len(p, b);
             nc = len.need - len.have;
             nt = len.fresh;
+            have[b] = len.have;
+            cached[b] = len.cached;
             if (rank == 0 && len.bad) flag(p.status, LSA_DEV_INDEX);
             if (rank == 0 && len.long_) flag(p.status, LSA_DEV_CAPACITY);
         }
@@ -213,25 +216,32 @@ __global__ void __launch_bounds__(CL_THREADS, 1) cluster_kernel(const Params p) 
     }
     cluster_barrier();      // the bitmap is clear
 
+    // Kept chunks: mark their slots and copy them; chunks past the need: -1.  (New ones follow.)
     const int turns = (p.stride + ROW - 1) / ROW;      // of a warp along one table row
     for (int item = gw; item < p.B * turns; item += WARPS) {
-        const int b = item / turns, c0 = (item - b * turns) * ROW;
-        const int have = Lengths(p, b).have;
+        const int b = item / turns, c0 = (item - b * turns) * ROW + lane;
+        const int keep = have[b], need = keep + base[b + 1] - base[b];
         const int32_t *row = p.table + (size_t)b * p.stride;
-        if (c0 >= have) continue;
-        int s[8];
+        int32_t *next = p.next + (size_t)b * p.stride;
+        int s[ROW / 32];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) s[i] = c0 + 32 * i + lane < have ? __ldg(row + c0 + 32 * i + lane) : 0;
+        for (int i = 0; i < ROW / 32; ++i) s[i] = c0 + 32 * i < keep ? __ldg(row + c0 + 32 * i) : -1;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            if (c0 + 32 * i + lane >= have) break;
-            if (s[i] >= 0 && s[i] < p.n_slots) atomicOr(&p.used[s[i] >> 5], 1u << (s[i] & 31));
-            else flag(p.status, LSA_DEV_TABLE);
+        for (int i = 0; i < ROW / 32; ++i) {
+            const int c = c0 + 32 * i;
+            if (c >= p.stride || (c >= keep && c < need)) continue;
+            if (s[i] >= 0 && s[i] < p.n_slots) {
+                atomicOr(&p.used[s[i] >> 5], 1u << (s[i] & 31));
+            } else {
+                if (c < keep) flag(p.status, LSA_DEV_TABLE);
+                s[i] = -1;
+            }
+            next[c] = s[i];
         }
     }
     cluster_barrier();      // every kept slot is marked
 
-    // free slots: each CTA counts its part of the bitmap, then lists those whose rank is needed
+    // Free slots: each CTA counts its part of the bitmap, then gives those whose rank is needed to the new chunks.
     const int per_cta = (words + CL - 1) / CL, w_lo = min(rank * per_cta, words), w_hi = min(w_lo + per_cta, words);
     auto free_bits = [&](int w) -> uint32_t {
         uint32_t bits = ~load_l2(p.used + w);
@@ -254,61 +264,61 @@ __global__ void __launch_bounds__(CL_THREADS, 1) cluster_kernel(const Params p) 
         if (r < rank) before += free_of[r];
         n_free += free_of[r];
     }
-    for (int w0 = w_lo; w0 < w_hi && before < chunks; w0 += CL_THREADS) {
-        const int w = w0 + t;
-        uint32_t bits = w < w_hi ? free_bits(w) : 0u;
+    // the last request whose first item is <= i, of B + 1 ascending entries
+    auto find = [&](const int *first, int i) {
+        int lo = 0, hi = p.B - 1;
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (first[mid] <= i) lo = mid;
+            else hi = mid - 1;
+        }
+        return lo;
+    };
+    auto give = [&](int r, int slot) {      // new chunk of rank r
+        const int b = find(base, r);
+        p.next[(size_t)b * p.stride + have[b] + r - base[b]] = slot;
+    };
+    // eight slots a thread: few enough that no thread gives many in a row
+    for (int u0 = 4 * w_lo; u0 < 4 * w_hi && before < chunks; u0 += CL_THREADS) {
+        const int u = u0 + t;
+        uint32_t bits = u < 4 * w_hi ? (free_bits(u >> 2) >> (8 * (u & 3))) & 0xffu : 0u;
         int tot;
         int r = before + block_exclusive_scan<CL_THREADS>(__popc(bits), warp_tot, &tot);
         while (bits && r < chunks) {
-            p.free_list[r++] = 32 * w + __ffs(bits) - 1;
+            give(r++, 8 * u + __ffs(bits) - 1);
             bits &= bits - 1;
         }
         before += tot;
     }
+    for (int r = n_free + gt; r < chunks; r += ALL) give(r, -1);
     if (gt == 0) {
         p.n_free[0] = max(n_free - chunks, 0);
         if (n_free < chunks || tokens > p.max_new) flag(p.status, LSA_DEV_CAPACITY);
     }
     for (int b = gt; b <= p.B; b += ALL) p.offset[b] = first_token[b];
-    if (chunks > 0) cluster_barrier();      // the list is written (uniform: every CTA has the same count)
+    if (p.max_new == 0) return;             // uniform
+    cluster_barrier();      // the next tables are written
 
-    auto slot_at = [&](int b, int c, const Lengths &len) -> int {
-        if (c < len.have) {
-            const int s = __ldg(p.table + (size_t)b * p.stride + c);
-            return s >= 0 && s < p.n_slots ? s : -1;
-        }
-        const int r = base[b] + c - len.have;
-        return c < len.need && r < n_free ? __ldcg(p.free_list + r) : -1;
-    };
-    for (int item = gw; item < p.B * turns; item += WARPS) {
-        const int b = item / turns, c0 = (item - b * turns) * ROW;
-        const Lengths len(p, b);
-        const int c_end = min(p.stride, c0 + ROW);
-        int s[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) s[i] = c0 + 32 * i + lane < c_end ? slot_at(b, c0 + 32 * i + lane, len) : -1;
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (c0 + 32 * i + lane < c_end) p.next[(size_t)b * p.stride + c0 + 32 * i + lane] = s[i];
-    }
     const int total = first_token[p.B];
-    for (int i = gt; i < p.max_new; i += ALL) {
-        int64_t slot = -1;
-        int pos = -1;
-        if (i < total) {
-            int lo = 0, hi = p.B - 1;      // the last request whose first token is <= i
-            while (lo < hi) {
-                const int mid = (lo + hi + 1) >> 1;
-                if (first_token[mid] <= i) lo = mid;
-                else hi = mid - 1;
+    for (int i0 = gt; i0 < p.max_new; i0 += 4 * ALL) {
+        int pos[4], s[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int i = i0 + j * ALL;
+            pos[j] = s[j] = -1;
+            if (i < total && i < p.max_new) {
+                const int b = find(first_token, i);
+                pos[j] = cached[b] + (i - first_token[b]);
+                if (pos[j] / LSA_CHUNK < p.stride) s[j] = __ldcg(p.next + (size_t)b * p.stride + pos[j] / LSA_CHUNK);
             }
-            const Lengths len(p, lo);
-            pos = len.cached + (i - first_token[lo]);
-            const int s = pos / LSA_CHUNK < p.stride ? slot_at(lo, pos / LSA_CHUNK, len) : -1;
-            if (s >= 0) slot = (int64_t)s * LSA_CHUNK + pos % LSA_CHUNK;
         }
-        p.slot_map[i] = slot;
-        p.position[i] = pos;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int i = i0 + j * ALL;
+            if (i >= p.max_new) break;
+            p.slot_map[i] = s[j] >= 0 ? (int64_t)s[j] * LSA_CHUNK + pos[j] % LSA_CHUNK : -1;
+            p.position[i] = pos[j];
+        }
     }
 }
 
