@@ -60,9 +60,8 @@ struct __align__(1024) Smem {
     uint64_t pv_full[2];                // the even CTA's, 16 arrivals: V and P of unit a of the tile are written
     uint64_t pv_done[2];                // P V over unit a is done: its V and P may be rewritten
     uint64_t s_full[2];                 // S buffers
-    uint64_t s_last;                    // Q K^T of the last tile is done
     uint64_t info_full[INFO];
-    uint64_t mma_done;
+    uint64_t mma_done;                  // all MMAs are done
     uint64_t never;                     // no arrival ever: the failure-path test's wait
     alignas(16) uint16_t mask[INFO][DEQ];           // present rows of a tile, 16 a word
     float qmul[HPC];                    // per head: score factor, scale * log2(e) * k_scale * 2^e
@@ -207,7 +206,6 @@ __global__ void __launch_bounds__(THREADS, 1) q4_mla_kernel(const DecodeParams p
             mbar_init(&sm.s_full[i], 1);
         }
         for (int i = 0; i < INFO; ++i) mbar_init(&sm.info_full[i], DEQ);
-        mbar_init(&sm.s_last, 1);
         mbar_init(&sm.mma_done, 1);
         mbar_init(&sm.never, 1);
         sm.abort_flag = 0;
@@ -350,7 +348,6 @@ __global__ void __launch_bounds__(THREADS, 1) q4_mla_kernel(const DecodeParams p
                         umma_commit_pair(&sm.k_empty[g], 0x3);
                     }
                     umma_commit_pair(&sm.s_full[sb], 0x3);
-                    if (n == n_tiles - 1) umma_commit_pair(&sm.s_last, 0x3);
                 }
                 __syncwarp();
             }
@@ -554,14 +551,9 @@ __global__ void __launch_bounds__(THREADS, 1) q4_mla_kernel(const DecodeParams p
 
     // ---- epilogue of O, by the 16 warps that dequantised (four column blocks at a time)
     if (warp >= 8) {
-        // A parity tells the last two phases apart, no more, so the last P V is waited for in step: Q K^T of the last
-        // tile comes after P V of tile n - 3, then tiles n - 2 and n - 1 in turn.
-        bool ok = n_tiles == 0 || warp_wait(sm, &sm.s_last, 0, p.status);
-#pragma unroll 1
-        for (int i = 0; i < 4 && n_tiles > 0 && ok; ++i) {
-            const int u = n_tiles - 2 + (i >> 1);
-            if (u >= 0) ok = warp_wait(sm, &sm.pv_done[i & 1], u & 1, p.status);
-        }
+        // Not pv_done: these warps do not wait for it tile by tile (K's never, V's only for their own unit), and a
+        // parity that is asked for once the next phase is over as well reads as not yet done.
+        if (n_tiles > 0) warp_wait(sm, &sm.mma_done, 0, p.status);
         tc_fence_after();
         // O leaves tensor memory 32 columns at a time and passes through shared memory (the K buffer, free now),
         // so that every store instruction writes whole 128-byte row pieces.

@@ -403,3 +403,22 @@ def test_latent_wait_that_runs_out(L):
     again = _run(L, c, st=st)
     assert st.item() == 0
     assert torch.equal(again[0], good[0]) and torch.equal(again[1], good[1])
+
+
+def test_latent_tails_with_cold_caches(L):
+    """One to five tiles a split, gathered rows first or last, nothing in the caches: the kernel's warps reach its
+    end far apart, and no wait may run out."""
+    flush = torch.empty(2 ** 26, dtype=torch.int32, device="cuda")
+    for n, (k, n_seq) in enumerate([(0, 74), (64, 74), (200, 74), (0, 37)]):
+        rng = np.random.default_rng(n)
+        starts = rng.integers(0, 400, n_seq) * (k > 0)
+        lengths = rng.integers(0, 640, n_seq)
+        c = _case(50 + n, n_seq, 128, 1, 576, 512, True, k, starts, lengths)
+        st, first = status(), None
+        for _ in range(4):
+            flush.zero_()
+            out, lse = _run(L, c, st=st)
+            first = first or (out, lse)
+            assert torch.equal(out, first[0]) and torch.equal(lse, first[1])
+        assert st.item() == 0
+        _check(c, *first)
