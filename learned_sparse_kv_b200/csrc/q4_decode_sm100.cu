@@ -41,7 +41,7 @@ constexpr int HPC = 64, HQ = 128;       // heads per CTA, per cluster
 constexpr int DQK = 576, DV = 512;
 constexpr int KCH = DQK / 64;           // 9 column chunks of 64
 constexpr int TILE = 128;
-constexpr int KG = 3, KPG = KCH / KG;    // K in three groups of three chunks
+constexpr int KG = 3;                   // K in groups of 256, 256 and 64 columns
 constexpr int INFO = 4;                 // row-mask ring
 constexpr int THREADS = 768, DEQ = 8;    // DEQ: warps of each dequantising group
 constexpr int ROW_CODE = DQK / 2, ROW_SCALE = DQK / 16;      // 288, 36 bytes
@@ -123,20 +123,25 @@ __host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, bool b_mn_maj
            (uint32_t(M >> 4) << 24);
 }
 
-// The 16 codes of one group with their scale byte -> two 16-byte units of eight f16 values, at the
-// addresses row + off0 and row + off1 (the swizzled places of two neighbouring units).
-__device__ __forceinline__ void store_group(uint32_t row, uint32_t off0, uint32_t off1, const uint2 &c, uint32_t scale) {
-    const uint32_t s = q4::dup_lo(q4::e4m3x2_to_f16(scale));
+// Eight codes times a scale -> one 16-byte unit of f16 values.
+__device__ __forceinline__ void store_unit(uint32_t at, uint32_t codes, uint32_t scale2) {
+    uint32_t h[4];
+    q4::e2m1x8_to_f16(codes, h);
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        uint32_t h[4];
-        q4::e2m1x8_to_f16(i ? c.y : c.x, h);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) h[j] = q4::hmul2(h[j], s);
-        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(row + (i ? off1 : off0)), "r"(h[0]), "r"(h[1]),
-                     "r"(h[2]), "r"(h[3])
-                     : "memory");
-    }
+    for (int j = 0; j < 4; ++j) h[j] = q4::hmul2(h[j], scale2);
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(h[0]), "r"(h[1]), "r"(h[2]), "r"(h[3]) : "memory");
+}
+
+// 32 columns of a row, a half of a 64-column chunk: four units at `at` ^ 16 i.  Lanes of odd chunks (`odd`) hand in
+// the address of their third unit and take the second group first, so that eight neighbouring lanes (two
+// rows of 128 columns) store to all banks.
+__device__ __forceinline__ void store_half(uint32_t at, bool odd, const uint4 &c, uint32_t scales) {
+    const uint32_t s = q4::e4m3x2_to_f16(scales);
+    const uint32_t s0 = __byte_perm(s, 0, odd ? 0x3232 : 0x1010), s1 = __byte_perm(s, 0, odd ? 0x1010 : 0x3232);
+    store_unit(at, odd ? c.z : c.x, s0);
+    store_unit(at ^ 16, odd ? c.w : c.y, s0);
+    store_unit(at ^ 32, odd ? c.x : c.z, s1);
+    store_unit(at ^ 48, odd ? c.y : c.w, s1);
 }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -168,21 +173,25 @@ __device__ __forceinline__ int64_t pool_row(const DecodeParams &p, int pos, int 
     return -1;
 }
 
-// A lane's place in a pool row: its group of 16 in every 64 columns.  An absent row reads the
-// pool's first row and gets zero scales, which make it zeros whatever it holds.
+// A pool row.  Four lanes share it, lane `quarter` takes 32 of every 128 columns, and 16 of the last 64 of a key.
+// An absent row reads the pool's first row and gets zero scales, which make it zeros whatever it holds.
 struct RowPtr {
     const uint8_t *code, *scale;
     bool there;
-    __device__ RowPtr(const uint8_t *pool, int64_t row, int quarter) {
+    __device__ RowPtr(const uint8_t *pool, int64_t row) {
         there = row >= 0;
         const uint8_t *chunk = pool + (there ? row >> 6 : 0) * q4::chunk_bytes(DQK);
         const int r = there ? (int)(row & 63) : 0;
-        code = chunk + r * ROW_CODE + quarter * 8;
-        scale = chunk + LSA_CHUNK * ROW_CODE + r * ROW_SCALE + quarter;
+        code = chunk + r * ROW_CODE;
+        scale = chunk + LSA_CHUNK * ROW_CODE + r * ROW_SCALE;
     }
-    __device__ __forceinline__ void load(int chunk, uint2 &c, uint32_t &s) const {
-        c = __ldg(reinterpret_cast<const uint2 *>(code + 32 * chunk));
-        s = there ? (uint32_t)__ldg(scale + 4 * chunk) : 0u;
+    __device__ __forceinline__ void load(int block, int quarter, uint4 &c, uint32_t &s) const {
+        c = __ldg(reinterpret_cast<const uint4 *>(code + 64 * block + 16 * quarter));
+        s = there ? (uint32_t)__ldg(reinterpret_cast<const uint16_t *>(scale + 8 * block + 2 * quarter)) : 0u;
+    }
+    __device__ __forceinline__ void load_last(int quarter, uint2 &c, uint32_t &s) const {
+        c = __ldg(reinterpret_cast<const uint2 *>(code + 256 + 8 * quarter));
+        s = there ? (uint32_t)__ldg(scale + 32 + quarter) : 0u;
     }
 };
 
@@ -213,29 +222,30 @@ __global__ void __launch_bounds__(THREADS, 1) q4_mla_kernel(const DecodeParams p
     }
     if (warp == 2) tmem_alloc_pair(&sm.tmem_base, TM_COLS);
     // ---- the dequantising warps look up and load their part of the first tile
-    // K: unit `rank` of each tile, 8 rows a warp, all nine column chunks.  V: all rows of the tile, 16 a warp
-    // in two passes of 8, this CTA's four chunks.  Four lanes share a row, each takes 16 columns of
-    // a chunk, so that the shared stores of eight lanes touch all banks.  Lane i looks up row i of the warp's.
+    // K: unit `rank` of each tile, 8 rows a warp, all columns.  V: all rows of the tile, 16 a warp in
+    // two passes of 8, this CTA's two blocks of 128 columns.  Lane i looks up row i of the warp's.
     const bool kwarp = warp >= 8 && warp < 16, vwarp = warp >= 16;
     const int w = warp & 7, quarter = lane & 3;
     const int unit_in_tile = kwarp ? (int)rank : w >> 2, first_row = kwarp ? 8 * w : 16 * (w & 3);   // in that unit
     auto position = [&](int u) -> int {
         return u < n_tiles ? row_position(un, p, b, 2 * tile_of(u) + unit_in_tile, first_row + (lane & (kwarp ? 7 : 15))) : ABSENT;
     };
-    uint2 c[KCH];
-    uint32_t sc[KCH];
+    uint4 c[4];          // K: the four blocks of 128 columns; V: block i >> 1, row pass i & 1
+    uint2 c_last;        // K: columns 512..575
+    uint32_t sc[5];
     int pos1 = ABSENT, pos2 = ABSENT, slot1 = -1;     // of tiles u + 1 and u + 2 in the loops below
     auto load = [&](int64_t r) {
         if (kwarp) {
-            const RowPtr row(p.k_pool, __shfl_sync(0xffffffffu, r, lane >> 2), quarter);
+            const RowPtr row(p.k_pool, __shfl_sync(0xffffffffu, r, lane >> 2));
 #pragma unroll
-            for (int i = 0; i < KCH; ++i) row.load(i, c[i], sc[i]);
+            for (int i = 0; i < 4; ++i) row.load(i, quarter, c[i], sc[i]);
+            row.load_last(quarter, c_last, sc[4]);
         } else {
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
-                const RowPtr row(p.k_pool, __shfl_sync(0xffffffffu, r, 8 * q + (lane >> 2)), quarter);
+                const RowPtr row(p.k_pool, __shfl_sync(0xffffffffu, r, 8 * q + (lane >> 2)));
 #pragma unroll
-                for (int i = 0; i < 4; ++i) row.load(4 * (i >> 1) + 2 * (int)rank + (i & 1), c[2 * i + q], sc[2 * i + q]);
+                for (int j = 0; j < 2; ++j) row.load(2 * j + (int)rank, quarter, c[2 * j + q], sc[2 * j + q]);
             }
         }
     };
@@ -259,14 +269,16 @@ __global__ void __launch_bounds__(THREADS, 1) q4_mla_kernel(const DecodeParams p
         slot1 = row_slot(p, b, pos1);
         row0 = pool_row(p, pos0, slot0);
         load(row0);
-    } else if (n_tiles > 0) {
-        // ---- warps 0..7: queries as f16 over a power of two, straight into the operand layout, four heads at a time
+    }
+    if (n_tiles > 0) {
+        // ---- queries as f16 over a power of two, straight into the operand layout: four heads each by warps 0..7,
+        // two by the others, whose codes are under way
         const uint32_t qb = smem_addr(sm.q);
 #pragma unroll 1
-        for (int h0 = 8 * warp; h0 < 8 * warp + 8; h0 += 4) {
-        uint4 held[4][3];
+        for (int h0 = warp < 8 ? 4 * warp : 16 + 2 * warp, h1 = h0 + (warp < 8 ? 4 : 2); h0 < h1; h0 += 2) {
+        uint4 held[2][3];
 #pragma unroll
-        for (int n = 0; n < 4; ++n) {
+        for (int n = 0; n < 2; ++n) {
             const int head = HPC * (int)rank + h0 + n;
             const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.q) + ((size_t)b * p.Hq + head) * DQK);
 #pragma unroll
@@ -274,7 +286,7 @@ __global__ void __launch_bounds__(THREADS, 1) q4_mla_kernel(const DecodeParams p
                 held[n][i] = head < p.Hq && lane + 32 * i < DQK / 8 ? __ldg(src + lane + 32 * i) : make_uint4(0, 0, 0, 0);
         }
 #pragma unroll
-        for (int n = 0; n < 4; ++n) {
+        for (int n = 0; n < 2; ++n) {
             const int h = h0 + n;
             const uint4 (&raw)[3] = held[n];
             float x[3][8];
@@ -312,6 +324,7 @@ __global__ void __launch_bounds__(THREADS, 1) q4_mla_kernel(const DecodeParams p
         }
         fence_proxy_async_smem();
     }
+    __syncwarp();          // the barriers take converged warps
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -339,7 +352,7 @@ __global__ void __launch_bounds__(THREADS, 1) q4_mla_kernel(const DecodeParams p
 #pragma unroll 1
                     for (int g = 0; g < KG; ++g) {
 #pragma unroll 1
-                        for (int c = KPG * g; c < KPG * (g + 1); ++c) {
+                        for (int c = 4 * g; c < min(4 * (g + 1), KCH); ++c) {
                             const uint64_t at = CHUNK * c;
 #pragma unroll
                             for (int kk = 0; kk < 4; ++kk)
@@ -373,16 +386,24 @@ __global__ void __launch_bounds__(THREADS, 1) q4_mla_kernel(const DecodeParams p
     } else if (kwarp && n_tiles > 0) {
         // ------------------------------------------------ dequantise K
         const int row = first_row + (lane >> 2);
-        const uint32_t dst = smem_addr(sm.k) + row * 128, full = map_to_rank(&sm.k_full, 0);
-        const uint32_t off0 = ((2 * quarter) ^ (row & 7)) << 4, off1 = off0 ^ 16;
+        const bool odd = quarter >> 1;
+        const uint32_t rows = smem_addr(sm.k) + row * 128, full = map_to_rank(&sm.k_full, 0);
+        const uint32_t at = rows + odd * (64 * 128) + (((4 * (quarter & 1) + 2 * odd) ^ (row & 7)) << 4);
+        const uint32_t at_last = rows + 8 * (64 * 128) + (((2 * quarter) ^ (row & 7)) << 4);
         bool ok = true;
         for (int u = 0; u < n_tiles && ok; ++u) {
 #pragma unroll
             for (int g = 0; g < KG; ++g) {
                 if (u > 0) ok = ok && warp_wait(sm, &sm.k_empty[g], (u - 1) & 1, p.status);
                 if (!ok) break;
-#pragma unroll
-                for (int i = KPG * g; i < KPG * (g + 1); ++i) store_group(dst + i * (64 * 128), off0, off1, c[i], sc[i]);
+                if (g < 2) {
+                    store_half(at + 4 * g * (64 * 128), odd, c[2 * g], sc[2 * g]);
+                    store_half(at + (4 * g + 2) * (64 * 128), odd, c[2 * g + 1], sc[2 * g + 1]);
+                } else {
+                    const uint32_t s2 = q4::dup_lo(q4::e4m3x2_to_f16(sc[4]));
+                    store_unit(at_last, c_last.x, s2);
+                    store_unit(at_last ^ 16, c_last.y, s2);
+                }
             }
             if (!ok) break;
             fence_proxy_async_smem();
@@ -396,8 +417,9 @@ __global__ void __launch_bounds__(THREADS, 1) q4_mla_kernel(const DecodeParams p
     } else if (vwarp && n_tiles > 0) {
         // ------------------------------------------------ dequantise V, post the row masks
         const int row = 16 * w + (lane >> 2);
-        const uint32_t dst = smem_addr(sm.v) + row * 128, full = map_to_rank(&sm.pv_full[w >> 2], 0);
-        const uint32_t off0 = ((2 * quarter) ^ (row & 7)) << 4, off1 = off0 ^ 16;
+        const bool odd = quarter >> 1;
+        const uint32_t full = map_to_rank(&sm.pv_full[w >> 2], 0);
+        const uint32_t at = smem_addr(sm.v) + row * 128 + odd * (TILE * 128) + (((4 * (quarter & 1) + 2 * odd) ^ (row & 7)) << 4);
         bool ok = true;
         post_mask(0, row0);
         for (int u = 0; u < n_tiles && ok; ++u) {
@@ -406,8 +428,8 @@ __global__ void __launch_bounds__(THREADS, 1) q4_mla_kernel(const DecodeParams p
             if (u > 0) ok = warp_wait(sm, &sm.pv_done[w >> 2], (u - 1) & 1, p.status);
             if (!ok) break;
 #pragma unroll
-            for (int i = 0; i < 8; ++i)       // chunk i >> 1, rows row and row + 8
-                store_group(dst + (i >> 1) * (TILE * 128) + (i & 1) * 1024, off0, off1, c[i], sc[i]);
+            for (int i = 0; i < 4; ++i)       // rows row and row + 8
+                store_half(at + (i >> 1) * (2 * TILE * 128) + (i & 1) * 1024, odd, c[i], sc[i]);
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive_cluster(full);
@@ -436,6 +458,7 @@ __global__ void __launch_bounds__(THREADS, 1) q4_mla_kernel(const DecodeParams p
             }
             if (ok) ok = wait_for(&sm.s_full[s], (u >> 1) & 1, &sm.abort_flag);
             if (!ok && *(volatile int *)&sm.abort_flag == 0) set_abort(sm, p.status);
+            __syncwarp();
             tc_fence_after();
             // Two passes over S (maximum, then weights), 32 columns at a time: 64 scores at once
             // would not fit the registers of 24 warps.  The factor is positive, so the
@@ -459,6 +482,7 @@ __global__ void __launch_bounds__(THREADS, 1) q4_mla_kernel(const DecodeParams p
             }
             float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * mul;
             sm.red[u & 1][L] = mx;
+            __syncwarp();
             named_barrier(1, 128);
             mx = fmaxf(mx, sm.red[u & 1][L ^ 64]);
             const bool move = mx > m_ref + q4::RESCALE;
@@ -536,9 +560,11 @@ __global__ void __launch_bounds__(THREADS, 1) q4_mla_kernel(const DecodeParams p
             ok = wait_for(&sm.pv_done[a], (n_tiles - 1) & 1, &sm.abort_flag);
             if (!ok && *(volatile int *)&sm.abort_flag == 0) set_abort(sm, p.status);
         }
+        __syncwarp();
         tc_fence_after();
         named_barrier(1, 128);
         sm.red[0][L] = l;
+        __syncwarp();
         named_barrier(1, 128);
         const float l_tot = l + sm.red[0][L ^ 64];
         const int head = HPC * (int)rank + h;
@@ -595,6 +621,7 @@ __global__ void __launch_bounds__(THREADS, 1) q4_mla_kernel(const DecodeParams p
         if (lane == 0 && !mbar_wait(&sm.mma_done, 0, WAIT_NS)) set_abort(sm, p.status);
         __syncwarp();
     }
+    __syncwarp();
     __syncthreads();
     cluster_sync();
     if (warp == 2) {
