@@ -21,6 +21,9 @@ run on the side stream during window w's steps (the lookahead pipeline): only
 chunks that are not already resident move, and the next table replaces the
 current one at the window boundary.  All buffers are allocated once, so step
 loops can be captured in CUDA graphs.
+
+With 4-bit pools (uint8) a step appends with lsa_append_token_q4 and attends with lsa_sparse_decode_q4;
+the indexer's keys stay bf16.
 """
 from dataclasses import dataclass
 from typing import Dict, List, Optional
@@ -56,10 +59,12 @@ class Window:
       q_nmi [B,Hn,dn], w_nmi [B,Hn], khat [sum n_ch, dn] bf16; seq_chunk_offset [B+1] int64
       nmi_union (optional): list of (q, w, khat) of several indexers gated in OR mode
       nmi_windows (optional, cold): per window (q, w, khat, seq_chunk_offset) of its gate
-      kv or k+v pools [slots,64,w] bf16, li pool [slots,64,dl] bf16
+      kv or k+v pools [slots,64,w] bf16, or 4-bit [slots,heads,36*w] uint8 (hot pools only; optional pool
+        scales k_scale, v_scale: floats); li pool [slots,64,dl] bf16
       chunk_table [B, stride] int32; window_start [B] int32
       per-step inputs stacked on dim 0 (windows x steps of them): q_li [S,B,Hl,dl], w_li [S,B,Hl],
-      q [S,B,Hq,dqk], new_k [S,B,dqk], new_v [S,B,dv] (separate layout), new_li [S,B,dl]
+      q [S,B,Hq,dqk], new_li [S,B,dl], and the new token's rows: new_kv [S,B,dqk] (latent), or new_k [S,B,dqk] and
+        new_v [S,B,dv] (separate layout; [S,B,heads,w] with 4-bit pools)
     cold: optional dict(host_pools=[pinned tensors], dev_pools=[device pools], first_window_chunk)
       for a batch-1 cold pool.
     """
@@ -100,11 +105,17 @@ class Window:
         self.ws_select = torch.empty(sel_ws, dtype=torch.uint8, device=d)
         self.scores = torch.empty(B, kept_cap * CHUNK, dtype=torch.float32, device=d)
         self.ws_topk = torch.empty(max(lsa.topk_workspace_size(B, kept_cap), 256), dtype=torch.uint8, device=d)
-        self.ws_decode = torch.empty(max(lsa.sparse_decode_workspace_size(B, shapes.Hq, shapes.dqk, shapes.dv,
-                                                                          shapes.k, self.max_window_len), 256),
-                                     dtype=torch.uint8, device=d)
         self.k_pool = t["kv"] if shapes.latent else t["k"]
         self.v_pool = None if shapes.latent else t["v"]
+        self.q4 = self.k_pool.dtype == torch.uint8
+        if self.q4:
+            assert not cold, "4-bit pools are hot"
+            self.q4_scales = dict(k_scale=float(t.get("k_scale", 1.0)), v_scale=float(t.get("v_scale", 1.0)))
+            dec_ws = lsa.sparse_decode_q4_workspace_size(B, shapes.Hq, self.k_pool.shape[1], shapes.dqk, shapes.dv,
+                                                         shapes.k, self.max_window_len)
+        else:
+            dec_ws = lsa.sparse_decode_workspace_size(B, shapes.Hq, shapes.dqk, shapes.dv, shapes.k, self.max_window_len)
+        self.ws_decode = torch.empty(max(dec_ws, 256), dtype=torch.uint8, device=d)
         self.graph = None
         self.graphs: List[torch.cuda.CUDAGraph] = []
         self.fetch_marks = None        # per window (plan start, fetch start, fetch end) events, when timing
@@ -163,7 +174,11 @@ class Window:
         """Decode step s of window w: append, indexer top-k, attention."""
         t, sh = self.t, self.s
         g = w * sh.steps + s
-        if sh.latent:
+        if self.q4:
+            lsa.append_token_q4(t["new_kv" if sh.latent else "new_k"][g], None if sh.latent else t["new_v"][g],
+                                t["new_li"][g], self.k_pool, self.v_pool, t["li"], t["chunk_table"],
+                                t["window_start"], self.window_len, status=self.status, **self.q4_scales)
+        elif sh.latent:
             lsa.append_topk(t["new_kv"][g], t["new_li"][g], self.k_pool, self.window_len, t["q_li"][g],
                             t["w_li"][g], t["li"], t["chunk_table"], self.kept_idx, self.kept_count,
                             t["window_start"], sh.k, scores=self.scores, status=self.status,
@@ -171,9 +186,16 @@ class Window:
         else:
             lsa.append_token(t["new_k"][g], t["new_v"][g], t["new_li"][g], self.k_pool, self.v_pool, t["li"],
                              t["chunk_table"], t["window_start"], self.window_len, status=self.status)
+        if self.q4 or not sh.latent:
             lsa.topk(t["q_li"][g], t["w_li"][g], t["li"], t["chunk_table"], self.kept_idx, self.kept_count,
                      t["window_start"], sh.k, scores=self.scores, status=self.status, topk_idx=self.topk_w[w, s],
                      topk_count=self.topk_count_w[w, s], ws=self.ws_topk)
+        if self.q4:
+            lsa.sparse_decode_q4(t["q"][g], self.k_pool, self.v_pool, t["chunk_table"], self.topk_w[w, s],
+                                 self.topk_count_w[w, s], t["window_start"], self.window_len, self.max_window_len,
+                                 sh.dv, sh.scale, out=self.out_w[w, s], lse=self.lse_w[w, s], status=self.status,
+                                 ws=self.ws_decode, **self.q4_scales)
+            return
         lsa.sparse_decode(t["q"][g], self.k_pool, self.v_pool, t["chunk_table"], self.topk_w[w, s],
                           self.topk_count_w[w, s], t["window_start"], self.window_len, self.max_window_len, sh.dv,
                           sh.scale, out=self.out_w[w, s], lse=self.lse_w[w, s], status=self.status,

@@ -19,7 +19,7 @@ def _nearest_even(x, table):
 
 def quantise(x, g=1.0):
     """float64 rows [..., W] -> (codes [..., W] 0..15, scale bytes [..., W / 16])."""
-    grp = x.reshape(x.shape[:-1] + (-1, 16))
+    grp = x.reshape(x.shape[:-1] + (x.shape[-1] // 16, 16))
     amax = np.abs(grp).max(-1)
     sb = _nearest_even(np.minimum(amax / (6.0 * g), 448.0), E4M3)
     s = E4M3[sb][..., None] * g
