@@ -450,7 +450,7 @@ int lsa_advance_window(int32_t *window_start, int32_t *window_len, int B, int by
  * Entries behind the last token are -1 in both, which lsa_qk_norm_rope and lsa_write_q4 skip,
  * so a batch may be padded to max_new rows.
  *
- *   table [B, table_stride] int32 (device); table_next the same shape, another buffer (out)
+ *   table [B, table_stride] int32 (device); table_next the same shape, not overlapping it (out)
  *   cached_len, new_len [B] int32 (device)
  *   slot_map [max_new] int64, position [max_new] int32 (device, out); new_offset [B + 1] int32 (device, out)
  *   n_free [1] int32 (device, out): slots still free
@@ -458,7 +458,7 @@ int lsa_advance_window(int32_t *window_start, int32_t *window_len, int B, int by
  * LSA_DEV_CAPACITY (too few free slots, a request longer than its table row, or more than
  * max_new new tokens: what does not fit gets -1 or no entry), LSA_DEV_INDEX (a negative
  * length, taken as 0).  A request is cut to 2^31 - 1 tokens, new_offset to 2^31 - 1.
- * Supported: 1 <= B <= 65535, table_stride < 2^25, n_slots < 2^31, max_new < 2^30.
+ * Supported: 1 <= B <= 65535, table_stride < 2^25, B * table_stride < 2^31, n_slots < 2^31, max_new < 2^30.
  */
 int lsa_build_tables(const int32_t *table, int table_stride, const int32_t *cached_len, const int32_t *new_len, int B,
                      int64_t n_slots, int max_new, int32_t *table_next, int64_t *slot_map, int32_t *position,
@@ -478,7 +478,8 @@ size_t lsa_build_tables_workspace_size(int B, int table_stride, int64_t n_slots)
  *     with `interleaved` rot_offset + 2 i and rot_offset + 2 i + 1
  * Angles are reduced in 64 bits, everything else is fp32, rounded once to the rows' type.
  * Rows whose position is negative are padding: nothing of them is read into a result and their
- * output rows stay as they are.  q_out may be q and k_out may be k.
+ * output rows stay as they are.  q_out may be q and k_out may be k; outputs must not overlap inputs
+ * in any other way.
  *   q, k, q_out, k_out: strides in elements for tokens and heads, columns contiguous; Hq or Hk may be 0
  *   weights [norm_width] of the rows' type; position [T] int32, inv_freq [rot_dim / 2] fp32 (device)
  * Supported: bf16, f16, fp32; even head_dim up to 1024; even rot_offset and rot_dim; up to 1024 heads.
@@ -549,8 +550,9 @@ int lsa_read_q4(const uint8_t *pool, int64_t n_slots, int heads, int width, floa
  *   max_window_len: host upper bound of window_len[b]; it sizes the split-K grid only
  * Softmax weights enter the value product as f16 (11 significant bits); scores, sums and
  * outputs accumulate in fp32.
- * dev_status: LSA_DEV_TABLE (a needed chunk has no valid slot: its rows are skipped),
- * LSA_DEV_INDEX (a negative position: skipped; a negative window_start: no window), LSA_DEV_TIMEOUT.
+ * dev_status: LSA_DEV_TABLE (a needed chunk has no valid slot, or the window is longer than its table
+ * row: its rows are skipped), LSA_DEV_INDEX (a negative position: skipped; a negative window_start: no
+ * window), LSA_DEV_TIMEOUT.
  * Supported: (dqk, dv) = (64, 64) or (128, 128) with separate pools and any Hq up to 1024 that is a
  * multiple of heads; (576, 512) latent with heads = 1 and 1 <= Hq <= 128.
  */

@@ -122,7 +122,7 @@ __device__ __forceinline__ uint32_t ld_shared_u8(uint32_t addr) {
 __device__ __forceinline__ int count_units(const DecodeParams &p, int b) {
     const int tk = p.k > 0 ? min(max(__ldg(p.topk_count + b), 0), p.k) : 0;
     const int start = __ldg(p.window_start + b);
-    const int len = start < 0 ? 0 : min(max(__ldg(p.window_len + b), 0), INT32_MAX - 63 - start);
+    const int len = window_rows(p, start, __ldg(p.window_len + b));
     return (tk + LSA_CHUNK - 1) / LSA_CHUNK + (len > 0 ? (start + len - 1) / LSA_CHUNK - start / LSA_CHUNK + 1 : 0);
 }
 
@@ -159,7 +159,8 @@ __global__ void __launch_bounds__(WARPS * 32, C::CTAS) q4_decode_kernel(const De
     for (int b = threadIdx.x; b < B; b += NT) {
         const int n = count_units(p, b);
         total += n > 0 ? n + SETUP : 0;
-        if (blockIdx.x == 0 && p.window_start[b] < 0 && p.window_len[b] > 0) flag(p.status, LSA_DEV_INDEX);
+        if (blockIdx.x == 0 && p.window_len[b] > window_rows(p, p.window_start[b], p.window_len[b]))
+            flag(p.status, p.window_start[b] < 0 ? LSA_DEV_INDEX : LSA_DEV_TABLE);
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);

@@ -23,6 +23,14 @@ struct DecodeParams {
     int q_f16, out_dtype;
 };
 
+// Window rows that a table row can hold: positions behind its last chunk have no slot, so a longer window is cut here
+// (and flagged) instead of being walked.
+__device__ __forceinline__ int window_rows(const DecodeParams &p, int start, int len) {
+    if (start < 0) return 0;
+    const int64_t end = lsa_min64((int64_t)p.table_stride * LSA_CHUNK, INT32_MAX - 63);
+    return (int)lsa_min64(max(len, 0), lsa_max64(end - start, 0));
+}
+
 // Units of one sequence: ceil(tk / 64) units of 64 top-k rows, then the window chunk by chunk
 // (its first and last chunk may be partly outside the window).
 struct Units {
@@ -30,12 +38,10 @@ struct Units {
     __device__ Units(const DecodeParams &p, int b) {
         tk = p.k > 0 ? min(max(p.topk_count[b], 0), p.k) : 0;
         wstart = p.window_start[b];
-        wlen = max(p.window_len[b], 0);
-        if (wstart < 0) {            // a window before position 0 does not exist
-            if (wlen > 0 && threadIdx.x == 0) flag(p.status, LSA_DEV_INDEX);
-            wstart = wlen = 0;
-        }
-        wlen = min(wlen, INT32_MAX - 63 - wstart);
+        const int len = p.window_len[b];
+        wlen = window_rows(p, wstart, len);
+        if (len > wlen && threadIdx.x == 0) flag(p.status, wstart < 0 ? LSA_DEV_INDEX : LSA_DEV_TABLE);
+        wstart = max(wstart, 0);     // a window before position 0 does not exist
         t_topk = (tk + LSA_CHUNK - 1) / LSA_CHUNK;
         first_chunk = wstart / LSA_CHUNK;
         total = t_topk + (wlen > 0 ? (wstart + wlen - 1) / LSA_CHUNK - first_chunk + 1 : 0);

@@ -422,3 +422,26 @@ def test_latent_tails_with_cold_caches(L):
             assert torch.equal(out, first[0]) and torch.equal(lse, first[1])
         assert st.item() == 0
         _check(c, *first)
+
+
+@pytest.mark.parametrize("Hq,heads,dqk,dv,latent", [(8, 2, 128, 128, False), (8, 1, 64, 64, False), (128, 1, 576, 512, True)])
+def test_windows_longer_than_their_table_row(L, Hq, heads, dqk, dv, latent):
+    """Rows behind the table row's last chunk do not exist: they are flagged and cost nothing, however many are asked for."""
+    c = _case(71, 5, Hq, heads, dqk, dv, latent, 64, [64, 128, 0, 64 * 9, 192], [300, 200, 5, 1, 100])
+    end = 64 * c["table"].shape[1]
+    c["table"][c["table"] < 0] = c["table"][0, 0]          # the spare chunk has a slot
+    real = dict(c, length=c["length"].copy(), start=c["start"].copy())
+    c["length"][0], real["length"][0] = 2 ** 31 - 1, end - 64
+    c["length"][1], real["length"][1] = end, end - 128
+    c["start"][3], c["length"][3], real["length"][3] = 2 ** 31 - 1, 2 ** 31 - 1, 0
+    c["start"][4], c["length"][4], real["length"][4] = end, 70, 0
+    for name in ("kp", "vp"):        # rows that only the longer windows have hold NaN scales: give them values
+        if c[name] is not None:
+            codes, scales = (a.copy() for a in R.unpack(c[name]))
+            scales[scales == 0x7f] = 0x30
+            c[name][...] = R.pack(codes, scales)
+    st = status()
+    out, lse = L.sparse_decode_q4(c["q"].cuda(), cu(c["kp"]), None if latent else cu(c["vp"]), cu(c["table"]), cu(c["topk"]),
+                                  cu(c["count"]), cu(c["start"]), cu(c["length"]), end, dv, c["scale"], status=st)
+    assert st.item() == L.DEV_TABLE
+    _check(dict(real, kp=c["kp"], vp=c["vp"]), out, lse)
