@@ -237,6 +237,7 @@ extern "C" int lsa_write_q4(int dtype, int64_t T, int heads, const void *k, int6
     if (two)
         if (int rc = check_side("lsa_write_q4", "v", b, dtype, T > 0)) return rc;
     LSA_REQUIRE(two || !v, LSA_ERR_INVALID_ARG, "lsa_write_q4: v without a v_pool");
+    LSA_REQUIRE(k_pool != v_pool, LSA_ERR_INVALID_ARG, "lsa_write_q4: k_pool and v_pool are the same");
     LSA_REQUIRE(slot_map || T == 0, LSA_ERR_INVALID_ARG, "lsa_write_q4: null pointer (slot_map)");
     if (T == 0) return LSA_OK;
     const int per_a = heads * (a.W / 8), per = per_a + (two ? heads * (b.W / 8) : 0);
@@ -276,6 +277,7 @@ extern "C" int lsa_append_token_q4(int dtype, int heads, const void *new_k, int 
     if (two)
         if (int rc = check_side("lsa_append_token_q4", "v", b, dtype, true)) return rc;
     LSA_REQUIRE(two || !new_v, LSA_ERR_INVALID_ARG, "lsa_append_token_q4: new_v without a v_pool");
+    LSA_REQUIRE(k_pool != v_pool, LSA_ERR_INVALID_ARG, "lsa_append_token_q4: k_pool and v_pool are the same");
     LSA_REQUIRE((li_pool != nullptr) == (new_li != nullptr) &&
                     (!li_pool || (dl >= 8 && dl % 8 == 0 && aligned16(new_li) && aligned16(li_pool))),
                 LSA_ERR_INVALID_ARG,

@@ -164,6 +164,7 @@ constexpr int CL = 16, CL_THREADS = 1024, CL_REQUESTS = 2048, CL_ENTRIES = 1 << 
 constexpr int ROW = 256;       // table entries of one warp's turn
 
 __device__ __forceinline__ void cluster_barrier() {
+    __syncwarp();           // the instructions take whole warps
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;\n" ::: "memory");
 }
 __device__ __forceinline__ uint32_t cta_of_cluster() {
@@ -377,7 +378,10 @@ extern "C" int lsa_build_tables(const int32_t *table, int table_stride, const in
     LSA_REQUIRE(table && cached_len && new_len && table_next && new_offset && n_free &&
                     (max_new == 0 || (slot_map && position)),
                 LSA_ERR_INVALID_ARG, "lsa_build_tables: null pointer");
-    LSA_REQUIRE(table != table_next, LSA_ERR_INVALID_ARG, "lsa_build_tables: table_next must not be table");
+    LSA_REQUIRE((int64_t)B * table_stride < (1ll << 31), LSA_ERR_INVALID_ARG,
+                "lsa_build_tables: a table of %lld entries (less than 2^31)", (long long)B * table_stride);
+    LSA_REQUIRE(table + (size_t)B * table_stride <= table_next || table_next + (size_t)B * table_stride <= table,
+                LSA_ERR_INVALID_ARG, "lsa_build_tables: table_next must not be table or overlap it");
     const size_t need = lsa_build_tables_workspace_size(B, table_stride, n_slots);
     LSA_REQUIRE(ws && ws_bytes >= need, LSA_ERR_WORKSPACE, "lsa_build_tables: workspace of %zu bytes, %zu needed",
                 ws_bytes, need);

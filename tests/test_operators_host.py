@@ -139,3 +139,11 @@ def test_the_binding_refuses_cpu_tensors():
         lsa.write_q4(torch.zeros(1, 1, 64), t, t)
     with pytest.raises(lsa.LSAError, match="CUDA"):
         lsa.sparse_decode_q4(torch.zeros(1, 1, 64), t, t, t, None, None, t, t, 1, 64, 1.0)
+
+
+def test_what_must_not_overlap():
+    refused(tables(nxt=P + 28), 1, "overlap")              # the table's last entry
+    refused(tables(nxt=P - 28), 1, "overlap")
+    refused(tables(B=65535, stride=40000, nxt=1 << 60, nws=1 << 40), 1, "2^31")
+    refused(write(v=P, vts=256, vhs=128, vw=128, vp=P), 1, "the same")
+    refused(append(v=P, vw=128, vp=P), 1, "the same")
