@@ -541,29 +541,39 @@ __global__ void __launch_bounds__(WARPS * 32, C::CTAS) q4_decode_kernel(const De
 }
 
 // One CTA per (sequence, query head) merges the parts of a segment that several CTAs share: the
-// weights of up to CH parts at a time, then D / 4 columns x MERGE / (D / 4) parts in flight.  It also answers for
-// sequences without rows (o = 0, lse = -inf).
+// weights of up to MERGE parts at a time, then D / 4 columns x ROWS parts in flight.  It also answers for
+// sequences without rows (o = 0, lse = -inf).  Nothing but latency: the range is read beside the lengths, and a
+// thread's first FLIGHT parts beside the maxima.
 constexpr int MERGE = 256;
 template <int D, int HPC>
 __global__ void __launch_bounds__(MERGE) q4_merge_split_kernel(const DecodeParams p) {
-    constexpr int COLS = D / 4, ROWS = MERGE / COLS;
+    constexpr int COLS = D / 4, ROWS = MERGE / COLS, FLIGHT = 16;
     __shared__ float4 red[ROWS][COLS];
     __shared__ float wmax[MERGE / 32], wsum[MERGE / 32], w_of[MERGE];
     const int b = blockIdx.y, head = blockIdx.x, G = p.Hq / p.heads, groups = (G + HPC - 1) / HPC;
     const int kvh = head / G, gh = head - kvh * G, grp = gh / HPC, h = gh - grp * HPC;
     const size_t row = (size_t)b * p.Hq + head;
     const int col = threadIdx.x % COLS, r = threadIdx.x / COLS;
+    const int2 range = p.seg_range[((size_t)b * p.heads + kvh) * groups + grp];     // anything if there are no units
     if (count_units(p, b) == 0) {
         if (r == 0) store_out(p, row * D + 4 * col, make_float4(0.f, 0.f, 0.f, 0.f));
         if (p.lse && threadIdx.x == 0) p.lse[row] = -INFINITY;
         return;
     }
-    const int2 range = p.seg_range[((size_t)b * p.heads + kvh) * groups + grp];
     if (range.x == range.y) return;            // finished by its CTA
     const int n = range.y - range.x + 1;
     auto part = [&](int i) { return (2 * (size_t)(range.x + i) + (i == 0 ? 1 : 0)) * HPC + h; };
-    float M = -INFINITY;
-    for (int i = threadIdx.x; i < n; i += MERGE) M = fmaxf(M, p.m_part[part(i)]);
+    float4 v[FLIGHT];
+#pragma unroll
+    for (int j = 0; j < FLIGHT; ++j)
+        if (r + j * ROWS < n) v[j] = __ldcs(reinterpret_cast<const float4 *>(p.o_part + part(r + j * ROWS) * D) + col);
+    float m0 = -INFINITY, l0 = 0.f;            // of this thread's first part
+    if (threadIdx.x < n) {
+        m0 = p.m_part[part(threadIdx.x)];
+        l0 = p.l_part[part(threadIdx.x)];
+    }
+    float M = m0;
+    for (int i = threadIdx.x + MERGE; i < n; i += MERGE) M = fmaxf(M, p.m_part[part(i)]);
     M = warp_max(M);
     if ((threadIdx.x & 31) == 0) wmax[threadIdx.x >> 5] = M;
     __syncthreads();
@@ -575,18 +585,26 @@ __global__ void __launch_bounds__(MERGE) q4_merge_split_kernel(const DecodeParam
         const int i = i0 + threadIdx.x;
         float f = 0.f;
         if (i < n) {
-            const float m = p.m_part[part(i)];
+            const float m = i0 == 0 ? m0 : p.m_part[part(i)], l = i0 == 0 ? l0 : p.l_part[part(i)];
             f = m == -INFINITY ? 0.f : exp2f(m - M);
-            L += f * p.l_part[part(i)];
+            L += f * l;
         }
         w_of[threadIdx.x] = f;
         __syncthreads();
         const int here = min(MERGE, n - i0);
-#pragma unroll 4
-        for (int j = r; j < here; j += ROWS) {
-            const float wgt = w_of[j];
-            const float4 v = __ldcs(reinterpret_cast<const float4 *>(p.o_part + part(i0 + j) * D) + col);
-            a.x += wgt * v.x; a.y += wgt * v.y; a.z += wgt * v.z; a.w += wgt * v.w;
+        for (int j0 = r; j0 < here; j0 += FLIGHT * ROWS) {
+            if (i0 + j0 != r) {
+#pragma unroll
+                for (int j = 0; j < FLIGHT; ++j)
+                    if (j0 + j * ROWS < here)
+                        v[j] = __ldcs(reinterpret_cast<const float4 *>(p.o_part + part(i0 + j0 + j * ROWS) * D) + col);
+            }
+#pragma unroll
+            for (int j = 0; j < FLIGHT; ++j)
+                if (j0 + j * ROWS < here) {
+                    const float wgt = w_of[j0 + j * ROWS];
+                    a.x += wgt * v[j].x; a.y += wgt * v[j].y; a.z += wgt * v[j].z; a.w += wgt * v[j].w;
+                }
         }
         __syncthreads();
     }
