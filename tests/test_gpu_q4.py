@@ -445,3 +445,57 @@ def test_windows_longer_than_their_table_row(L, Hq, heads, dqk, dv, latent):
                                   cu(c["count"]), cu(c["start"]), cu(c["length"]), end, dv, c["scale"], status=st)
     assert st.item() == L.DEV_TABLE
     _check(dict(real, kp=c["kp"], vp=c["vp"]), out, lse)
+
+
+@pytest.mark.parametrize("Hq,heads,dqk,dv,latent", [(8, 2, 128, 128, False), (40, 1, 64, 64, False), (16, 1, 576, 512, True)])
+def test_many_short_sequences(L, Hq, heads, dqk, dv, latent):
+    """More sequences than a block has threads, most of them empty or a few rows long, some with top-k rows alone."""
+    rng = np.random.default_rng(Hq)
+    B = 700
+    starts = rng.integers(0, 3, B) * rng.integers(0, 100, B)
+    lengths = rng.integers(0, 2, B) * rng.integers(0, 90, B)
+    starts[300:430] = lengths[300:430] = 0                     # a whole stretch of nothing
+    lengths[699] = 700
+    c = _case(81, B, Hq, heads, dqk, dv, latent, 30, starts, lengths)
+    st = status()
+    out, lse = _run(L, c, st=st)
+    assert st.item() == 0
+    _check(c, out, lse)
+
+
+@pytest.mark.parametrize("heads,dqk,dv,latent", [(8, 128, 128, False), (1, 576, 512, True)])
+def test_pools_past_32_bits(L, heads, dqk, dv, latent):
+    """Slots behind the first 4 GiB of a pool, and rows 2^31 elements apart, give what a small pool gives, bit for bit."""
+    n_big = 2 ** 32 // (heads * 36 * dqk) + 40
+    rng = np.random.default_rng(5)
+    T = 150
+    # rows more than 2^31 elements apart: three tokens of one buffer
+    wide = torch.zeros(2 ** 31 + 2 ** 21, dtype=torch.bfloat16, device="cuda")
+    rows = wide.as_strided((3, heads, dqk), (2 ** 30, dqk, 1))
+    rows.copy_(torch.from_numpy(rng.standard_normal((3, heads, dqk))))
+    k = torch.from_numpy(rng.standard_normal((T, heads, dqk))).to("cuda", torch.bfloat16)
+    k[:3] = rows
+    v = None if latent else torch.from_numpy(rng.standard_normal((T, heads, dv))).to("cuda", torch.bfloat16)
+    q = torch.from_numpy(rng.standard_normal((1, 16, dqk))).to("cuda", torch.bfloat16)
+    got = []
+    for n_slots, first in ((5, 1), (n_big, n_big - 4)):
+        kp = L.q4_pool(n_slots, heads, dqk)
+        vp = None if latent else L.q4_pool(n_slots, heads, dv)
+        table = torch.arange(first, first + 4, dtype=torch.int32, device="cuda")[None]
+        slots = first * CH + torch.arange(T, device="cuda")
+        st = status()
+        L.write_q4(k, kp, slots, v=v, v_pool=vp, status=st)
+        L.write_q4(rows, kp, slots[:3].clone(), status=st)     # the same values again, from far apart
+        start, length = (torch.tensor([x], dtype=torch.int32, device="cuda") for x in (0, T))
+        L.append_token_q4(k[7:8].contiguous(), None if latent else v[7:8].contiguous(), None, kp, vp, None, table, start,
+                          length, status=st)
+        topk = torch.tensor([[3, 70, 149]], dtype=torch.int32, device="cuda")
+        out, lse = L.sparse_decode_q4(q, kp, vp, table, topk, torch.tensor([3], dtype=torch.int32, device="cuda"), start,
+                                      length, T + 1, dv, 0.05, status=st)
+        back = L.read_q4(kp, torch.cat([slots, slots[-1:] + 1]), status=st)
+        assert st.item() == 0 and length.item() == T + 1
+        got.append((out, lse, back))
+        del kp, vp
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
+    assert torch.equal(got[0][2][7], got[0][2][T])
