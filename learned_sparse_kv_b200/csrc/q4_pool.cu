@@ -5,8 +5,8 @@
 // A thread owns half a group, eight values: 16 bytes of a bf16 row, 4 code bytes; the two lanes of a
 // group exchange their maxima.  A thread keeps its place in the row (side, head, columns) and walks
 // the tokens, so that no division is left in the loop.  2 + 0.5625 bytes a bf16 value would bound it by
-// memory; measured, 16,384 tokens of 8 heads of 128, K and V: write 28 us (86 MB, 3.1 of 6.55 TB/s), two reads of
-// 43 MB 12 us each, 49 us in all: the rounding takes about 9 instructions a value and the issue slots are busy.
+// memory; measured, 16,384 tokens of 8 heads of 128, K and V: 44 us in all for 172 MB,
+// 3.9 of 6.55 TB/s: the rounding takes about 9 instructions a value, and two thirds of the issue slots are busy.
 #include "nvtx_range.cuh"
 #include "q4.cuh"
 
@@ -40,17 +40,25 @@ struct Place {
     }
 };
 
+// Eight values as they are stored.
 template <class T>
-__device__ __forceinline__ void load8(const T *src, float (&x)[8]) {
-    constexpr int PER = 16 / sizeof(T);
+struct Raw8 {
+    static constexpr int PER = 16 / sizeof(T);
+    Vec<T, PER> v[8 / PER];
+    __device__ __forceinline__ void load(const T *src) {
 #pragma unroll
-    for (int i = 0; i < 8 / PER; ++i) {
-        float f[PER];
-        widen(*reinterpret_cast<const Vec<T, PER> *>(src + i * PER), f);
-#pragma unroll
-        for (int j = 0; j < PER; ++j) x[i * PER + j] = f[j];
+        for (int i = 0; i < 8 / PER; ++i) v[i] = *reinterpret_cast<const Vec<T, PER> *>(src + i * PER);
     }
-}
+    __device__ __forceinline__ void widen_to(float (&x)[8]) const {
+#pragma unroll
+        for (int i = 0; i < 8 / PER; ++i) {
+            float f[PER];
+            widen(v[i], f);
+#pragma unroll
+            for (int j = 0; j < PER; ++j) x[i * PER + j] = f[j];
+        }
+    }
+};
 
 // The whole warp calls; slot < 0: nothing is written.
 template <bool EXACT>
@@ -65,6 +73,7 @@ __device__ __forceinline__ void put_half(const Place &at, int64_t slot, const fl
 }
 
 // `per` half groups a token; where they are fewer than the block's threads, a block takes several tokens at once.
+constexpr int FLIGHT = 2;
 template <class T, bool EXACT>
 __global__ void __launch_bounds__(256) q4_write_kernel(const Q4Side a, const Q4Side b, int heads, int64_t T_, int per,
                                                        int per_a, int64_t n_rows, const int64_t *__restrict__ slot_map,
@@ -77,26 +86,33 @@ __global__ void __launch_bounds__(256) q4_write_kernel(const Q4Side a, const Q4S
         const Place at(a, b, live ? u : 0, per_a, heads);
         const T *src = static_cast<const T *>(at.s.x) + at.h * at.s.head_stride + at.col;
         const int64_t step = (int64_t)gridDim.x * tokens;
-        for (int64_t t0 = (int64_t)blockIdx.x * tokens; t0 < T_; t0 += 2 * step) {
-            // two tokens in flight
-            float x[2][8];
-            int64_t slot[2];
+        // FLIGHT tokens are worked on while the next FLIGHT are on their way
+        Raw8<T> raw[FLIGHT], next[FLIGHT];
+        int64_t slot[FLIGHT], slot_next[FLIGHT];
+        auto fetch = [&](int64_t t0, Raw8<T> (&r)[FLIGHT], int64_t (&sl)[FLIGHT]) {
 #pragma unroll
-            for (int n = 0; n < 2; ++n) {
+            for (int n = 0; n < FLIGHT; ++n) {
                 const int64_t t = t0 + mine + n * step;
-                slot[n] = -1;
-#pragma unroll
-                for (int j = 0; j < 8; ++j) x[n][j] = 0.f;
+                sl[n] = -1;
                 if (live && t < T_) {
-                    slot[n] = slot_map[t];
-                    load8(src + t * at.s.token_stride, x[n]);
+                    sl[n] = slot_map[t];
+                    r[n].load(src + t * at.s.token_stride);
                 }
             }
+        };
+        int64_t t0 = (int64_t)blockIdx.x * tokens;
+        fetch(t0, raw, slot);
+        for (; t0 < T_; t0 += FLIGHT * step) {
+            fetch(t0 + FLIGHT * step, next, slot_next);
 #pragma unroll
-            for (int n = 0; n < 2; ++n) {
+            for (int n = 0; n < FLIGHT; ++n) {
+                float x[8];
+                raw[n].widen_to(x);       // of a token behind the last: whatever is there, and not written
                 const bool there = (uint64_t)slot[n] < (uint64_t)n_rows;
                 if (!there && slot[n] != -1) flag(status, LSA_DEV_INDEX);
-                put_half<EXACT>(at, there ? slot[n] : -1, x[n]);
+                put_half<EXACT>(at, there ? slot[n] : -1, x);
+                raw[n] = next[n];
+                slot[n] = slot_next[n];
             }
         }
     }
@@ -127,7 +143,11 @@ __global__ void __launch_bounds__(256) q4_append_kernel(const Q4Side a, const Q4
         const bool live = u < per;
         const Place at(a, b, live ? u : 0, per_a, heads);
         float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-        if (live) load8(static_cast<const T *>(at.s.x) + seq * at.s.token_stride + at.h * at.s.head_stride + at.col, x);
+        if (live) {
+            Raw8<T> raw;
+            raw.load(static_cast<const T *>(at.s.x) + seq * at.s.token_stride + at.h * at.s.head_stride + at.col);
+            raw.widen_to(x);
+        }
         put_half<true>(at, live ? row : -1, x);
     }
     if (li_pool)
@@ -189,10 +209,10 @@ __global__ void __launch_bounds__(256) q4_read_kernel(const uint8_t *__restrict_
     }
 }
 
-// Blocks for T tokens of `per` half groups, `flight` tokens of a thread at a time: up to 16 a multiprocessor.
-static int q4_blocks(int64_t T, int per, int flight) {
+// Blocks for T tokens of `per` half groups, `flight` tokens of a thread at a time: up to `ctas` a multiprocessor.
+static int q4_blocks(int64_t T, int per, int flight, int ctas) {
     const int64_t tokens = per < 256 ? 256 / per : 1;
-    return (int)lsa_max64(1, lsa_min64((T + tokens * flight - 1) / (tokens * flight), (int64_t)sm_count() * 16));
+    return (int)lsa_max64(1, lsa_min64((T + tokens * flight - 1) / (tokens * flight), (int64_t)sm_count() * ctas));
 }
 
 static bool power_of_two(float g) {
@@ -245,13 +265,13 @@ extern "C" int lsa_write_q4(int dtype, int64_t T, int heads, const void *k, int6
     const int per_a = heads * (a.W / 8), per = per_a + (two ? heads * (b.W / 8) : 0);
     const int64_t rows = n_slots * LSA_CHUNK;
     // 16-bit rows and power-of-two scales need no division (quantise_half): 16,384 tokens of 8 heads, K and V, written
-    // and read back, 49 us instead of 58.
+    // and read back, took 49 us instead of 58.
     const bool exact = dtype == LSA_DTYPE_F32 || !power_of_two(k_scale) || (two && !power_of_two(v_scale));
     if (!exact) {
         a.g6 = 1.f / a.g6;
         if (two) b.g6 = 1.f / b.g6;
     }
-    const int blocks = q4_blocks(T, per, 2);
+    const int blocks = q4_blocks(T, per, FLIGHT, 3);     // what is resident: 44.1 us the case above; 5: 45.8, 16: 48.8
 #define LSA_WRITE(TYPE, E) q4_write_kernel<TYPE, E><<<blocks, 256, 0, stream>>>(a, b, heads, T, per, per_a, rows, slot_map, dev_status)
     if (dtype == LSA_DTYPE_F32) LSA_WRITE(float, true);
     else if (dtype == LSA_DTYPE_BF16 && exact) LSA_WRITE(__nv_bfloat16, true);
@@ -311,7 +331,7 @@ extern "C" int lsa_read_q4(const uint8_t *pool, int64_t n_slots, int heads, int 
                 "lsa_read_q4: the pool scale must be positive and between 1e-30 and 1e30");
     if (T == 0) return LSA_OK;
     const int64_t rows = n_slots * LSA_CHUNK;
-    const int blocks = q4_blocks(T, heads * (width / 8), 4);
+    const int blocks = q4_blocks(T, heads * (width / 8), 4, 5);     // 4 or 6: 46.7 us instead of 45.8, 16: 47.0
     if (out_dtype == LSA_DTYPE_BF16)
         q4_read_kernel<<<blocks, 256, 0, stream>>>(pool, heads, width, rows, slot_map, T, scale, static_cast<__nv_bfloat16 *>(out), dev_status);
     else if (out_dtype == LSA_DTYPE_F16)
