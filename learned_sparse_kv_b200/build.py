@@ -52,7 +52,7 @@ def _compile_binding():
 def _link_binding(obj):
     tmp = BINDING + f".tmp{os.getpid()}"
     cmd = [os.environ.get("CXX", "g++"), "-shared", "-o", tmp, obj, f"-L{HERE}", "-llsa", "-Wl,-rpath,$ORIGIN",
-           f"-L{os.path.join(_torch_dir(), 'lib')}", "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+           f"-L{os.path.join(_torch_dir(), 'lib')}", "-ltorch_python", "-ltorch", "-ltorch_cpu", "-ltorch_cuda", "-lc10", "-lc10_cuda"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link of the binding failed:\n{r.stderr}")

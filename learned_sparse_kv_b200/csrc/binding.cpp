@@ -9,6 +9,7 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
@@ -118,8 +119,9 @@ lsa_stream_t stream_of(PyObject *o, int index) {
     return reinterpret_cast<lsa_stream_t>(c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)index).stream());
 }
 
+// Without the dispatcher: half the time of at::empty, and a call makes up to six.
 at::Tensor fresh(at::IntArrayRef shape, at::ScalarType type, int index) {
-    return at::empty(shape, at::TensorOptions().dtype(type).device(at::kCUDA, (c10::DeviceIndex)index));
+    return at::detail::empty_cuda(shape, type, c10::Device(at::kCUDA, (c10::DeviceIndex)index), std::nullopt);
 }
 
 // A caller's workspace, or a new one of `bytes`.
