@@ -5,8 +5,12 @@ torch tensors (bf16 inputs as torch.bfloat16); the binding allocates outputs
 and workspaces with torch, passes raw pointers plus the current CUDA stream,
 and turns a non-zero status into an LSAError.  There is no CPU fallback: if
 the library is missing the import fails.
+
+With `stream=` a call runs on that stream, what it allocates included; ordering it
+after the work that makes its inputs, and what reads its outputs after it, is the caller's.
 """
 import ctypes
+import functools
 import importlib.machinery
 import importlib.util
 import os
@@ -118,6 +122,35 @@ def _stream(stream=None):
     return ctypes.c_void_p(s.cuda_stream)
 
 
+def _on_stream(stream, call, /, *args, **kwargs):
+    """call(...) with `stream` current, so that what it allocates comes from that stream's pool.
+
+    A block of the caller's pool may just have been freed with kernels that use it still queued on the caller's
+    stream, and nothing would order `stream` behind them.  The outputs are recorded for the caller's stream too:
+    one that is dropped while the caller's stream still reads it is not handed out before that is done.
+    """
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(stream.cuda_stream)
+    caller = torch.cuda.current_stream(stream.device)
+    with torch.cuda.stream(stream):
+        out = call(*args, **kwargs)
+    for t in out if isinstance(out, tuple) else (out,):
+        if isinstance(t, torch.Tensor) and t.is_cuda:
+            t.record_stream(stream)      # an output that the caller handed in belongs to another pool
+            t.record_stream(caller)
+    return out
+
+
+def _ordered(fn):
+    """A call that allocates runs as a whole on the stream it is given."""
+    @functools.wraps(fn)
+    def call(*args, stream=None, **kwargs):
+        if stream is None:
+            return fn(*args, **kwargs)
+        return _on_stream(stream, fn, *args, stream=stream, **kwargs)
+    return call
+
+
 def _dev(t, dtype, name):
     if not (isinstance(t, torch.Tensor) and t.is_cuda):
         raise LSAError(1, f"{name} must be a CUDA tensor")
@@ -140,6 +173,7 @@ def nmi_select_workspace_size(B, max_chunks_per_seq):
     return _lib.lsa_nmi_select_workspace_size(B, max_chunks_per_seq)
 
 
+@_ordered
 def nmi_select(q, w, khat, seq_chunk_offset, max_chunks_per_seq, kept_cap, *, logits=None, status=None,
                kept_idx=None, kept_count=None, ws=None, stream=None):
     """Chunk gate.  Returns (kept_idx [B, kept_cap] int32, kept_count [B] int32)."""
@@ -162,6 +196,7 @@ def nmi_select_union_workspace_size(n_idx, B, max_chunks_per_seq):
     return _lib.lsa_nmi_select_union_workspace_size(n_idx, B, max_chunks_per_seq)
 
 
+@_ordered
 def nmi_select_union(qs, ws_, khats, seq_chunk_offset, max_chunks_per_seq, kept_cap, *, logits=None, status=None,
                      kept_idx=None, kept_count=None, ws=None, stream=None):
     """OR-mode gate of several indexers (lists of q [B,Hn,dn], w [B,Hn], khat [sum n_ch, dn]).
@@ -192,6 +227,7 @@ def query_encoder_workspace_size(B, d_model, rank, Hn, dn):
     return _lib.lsa_query_encoder_workspace_size(B, d_model, rank, Hn, dn)
 
 
+@_ordered
 def query_encoder(h, w_down, w_up, w_head, Hn, dn, *, q_out=None, w_out=None, q_f32=None, w_f32=None, status=None,
                   ws=None, stream=None):
     """Indexer queries from hidden states: h [B, d_model] -> (q [B, Hn, dn] bf16, w [B, Hn] bf16)."""
@@ -221,6 +257,7 @@ def select_baseline_workspace_size(B, max_old_chunks):
     return _lib.lsa_select_baseline_workspace_size(B, max_old_chunks)
 
 
+@_ordered
 def select_baseline(mode, window_start, max_old_chunks, kept_cap, *, seed=0, keep_num=1, keep_den=10, status=None,
                     kept_idx=None, kept_count=None, ws=None, stream=None):
     """Recency-only (SELECT_RECENT) or random-fraction (SELECT_RANDOM) kept list in the gate's format.
@@ -250,6 +287,7 @@ def topk_kernel_count(B, Hl, dl):
     return _lib.lsa_topk_kernel_count(B, Hl, dl)
 
 
+@_ordered
 def topk(q_li, w_li, li_pool, chunk_table, kept_idx, kept_count, window_start, k, *, scores=None, status=None,
          topk_idx=None, topk_count=None, ws=None, stream=None):
     """Lightning-indexer scores + fine top-k.  Returns (topk_idx [B,k], topk_count [B])."""
@@ -271,6 +309,7 @@ def topk(q_li, w_li, li_pool, chunk_table, kept_idx, kept_count, window_start, k
     return topk_idx, topk_count
 
 
+@_ordered
 def append_topk(new_kv, new_li, kv_pool, window_len, q_li, w_li, li_pool, chunk_table, kept_idx, kept_count,
                 window_start, k, *, scores=None, status=None, topk_idx=None, topk_count=None, ws=None,
                 stream=None):
@@ -303,6 +342,7 @@ def append_topk_kernel_count(B, Hl, dl):
     return n if n == 2 else n + 1
 
 
+@_ordered
 def topk_from_scores(scores, cand_offset, max_cand, k, *, stream=None):
     """Exact top-k of given fp32 scores per segment.  Returns (idx [B,k], count [B])."""
     _dev(scores, torch.float32, "scores"); _dev(cand_offset, torch.int64, "cand_offset")
@@ -320,6 +360,7 @@ def sparse_decode_workspace_size(B, Hq, dqk, dv, k, max_window_len):
     return _lib.lsa_sparse_decode_workspace_size(B, Hq, dqk, dv, k, max_window_len)
 
 
+@_ordered
 def sparse_decode(q, k_pool, v_pool, chunk_table, topk_idx, topk_count, window_start, window_len, max_window_len,
                   dv, scale, *, out=None, lse=None, want_lse=True, status=None, ws=None, stream=None):
     """Attention over top-k rows + window.  k_pool [slots,64,Kw]; v_pool None (latent) or [slots,64,Vw].
@@ -348,6 +389,7 @@ def sparse_decode(q, k_pool, v_pool, chunk_table, topk_idx, topk_count, window_s
     return out, lse
 
 
+@_ordered
 def merge_attention(o_parts, lse_parts, *, out=None, lse=None, stream=None):
     """o_parts [R, B, Hq, dv], lse_parts [R, B, Hq] fp32 -> (out [B, Hq, dv], lse [B, Hq])."""
     _dev(o_parts, torch.float32, "o_parts"); _dev(lse_parts, torch.float32, "lse_parts")
@@ -404,6 +446,7 @@ def plan_residency_workspace_size(table_len, n_slots):
     return _lib.lsa_plan_residency_workspace_size(table_len, n_slots)
 
 
+@_ordered
 def plan_residency(table_cur, table_next, kept_idx, kept_count, first_window_chunk, window_end_chunk, n_slots,
                    copy_chunk, copy_slot, copy_count, *, status=None, ws=None, stream=None):
     """Next window's chunk table and copy list (device tensors, one sequence)."""
@@ -456,22 +499,6 @@ def _load_binding():
 _native = _load_binding()
 
 
-def _side_workspace(nbytes, first, stream):
-    """A workspace for work on a side stream: it stays reserved until that work is done."""
-    ws = torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device=getattr(first, "device", "cuda"))
-    if ws.is_cuda:
-        ws.record_stream(stream)
-    return ws
-
-
-def _on_side(stream, outputs):
-    """Outputs made on the current stream and written on `stream`."""
-    for t in outputs:
-        if t is not None:
-            t.record_stream(stream)
-    return outputs
-
-
 def build_tables_workspace_size(B, table_stride, n_slots):
     return _lib.lsa_build_tables_workspace_size(B, table_stride, n_slots)
 
@@ -484,13 +511,11 @@ def build_tables(table, cached_len, new_len, n_slots, max_new, *, table_next=Non
     slot_map [max_new] int64, position [max_new] int32, new_offset [B + 1] int32, n_free [1] int32); map entries behind
     the last new token are -1.
     """
-    if stream is None:
-        return _native.build_tables(table, cached_len, new_len, n_slots, max_new, table_next, slot_map, position,
-                                    new_offset, n_free, status, ws, None)
-    if ws is None:
-        ws = _side_workspace(build_tables_workspace_size(*table.shape, n_slots), table, stream)
-    return _on_side(stream, _native.build_tables(table, cached_len, new_len, n_slots, max_new, table_next, slot_map,
-                                                 position, new_offset, n_free, status, ws, stream.cuda_stream))
+    if stream is not None:
+        return _on_stream(stream, _native.build_tables, table, cached_len, new_len, n_slots, max_new, table_next, slot_map,
+                          position, new_offset, n_free, status, ws, stream.cuda_stream)
+    return _native.build_tables(table, cached_len, new_len, n_slots, max_new, table_next, slot_map, position,
+                                new_offset, n_free, status, ws, None)
 
 
 def qk_norm_rope(q, k, position, inv_freq, *, q_weight=None, k_weight=None, q_norm_width=None, k_norm_width=None,
@@ -502,11 +527,11 @@ def qk_norm_rope(q, k, position, inv_freq, *, q_weight=None, k_weight=None, q_no
     k_norm_width columns (default: the weight's length, or none without a weight); the rotation covers columns
     [rot_offset, rot_offset + rot_dim).  Returns (q_out, k_out); outputs may be the inputs.
     """
-    if stream is None:
-        return _native.qk_norm_rope(q, k, position, inv_freq, q_weight, k_weight, q_norm_width, k_norm_width, eps,
-                                    rot_offset, interleaved, q_out, k_out, None)
-    return _on_side(stream, _native.qk_norm_rope(q, k, position, inv_freq, q_weight, k_weight, q_norm_width, k_norm_width,
-                                                 eps, rot_offset, interleaved, q_out, k_out, stream.cuda_stream))
+    if stream is not None:
+        return _on_stream(stream, _native.qk_norm_rope, q, k, position, inv_freq, q_weight, k_weight, q_norm_width,
+                          k_norm_width, eps, rot_offset, interleaved, q_out, k_out, stream.cuda_stream)
+    return _native.qk_norm_rope(q, k, position, inv_freq, q_weight, k_weight, q_norm_width, k_norm_width, eps,
+                                rot_offset, interleaved, q_out, k_out, None)
 
 
 # ------------------------------------------------------- 4-bit pools ----
@@ -540,9 +565,9 @@ def append_token_q4(new_k, new_v, new_li, k_pool, v_pool, li_pool, chunk_table, 
 
 def read_q4(pool, slot_map, *, scale=1.0, out=None, out_dtype=torch.bfloat16, status=None, stream=None):
     """Rows slot_map [T] of a 4-bit pool as values [T, heads, width] (zeros where slot_map is -1)."""
-    if stream is None:
-        return _native.read_q4(pool, slot_map, scale, out, out_dtype, status, None)
-    return _on_side(stream, (_native.read_q4(pool, slot_map, scale, out, out_dtype, status, stream.cuda_stream),))[0]
+    if stream is not None:
+        return _on_stream(stream, _native.read_q4, pool, slot_map, scale, out, out_dtype, status, stream.cuda_stream)
+    return _native.read_q4(pool, slot_map, scale, out, out_dtype, status, None)
 
 
 def sparse_decode_q4_workspace_size(B, Hq, heads, dqk, dv, k, max_window_len):
@@ -557,17 +582,13 @@ def sparse_decode_q4(q, k_pool, v_pool, chunk_table, topk_idx, topk_count, windo
 
     Returns (out [B, Hq, dv] of out_dtype, lse [B, Hq] fp32 or None).
     """
-    if stream is None:
-        return _native.sparse_decode_q4(q, k_pool, v_pool, chunk_table, topk_idx, topk_count, window_start, window_len,
-                                        max_window_len, dv, scale, k_scale, v_scale, out, out_dtype, lse, want_lse, status,
-                                        ws, None)
-    if ws is None:
-        B, Hq, dqk = q.shape
-        k = 0 if topk_idx is None else topk_idx.shape[-1]
-        ws = _side_workspace(sparse_decode_q4_workspace_size(B, Hq, k_pool.shape[1], dqk, dv, k, max_window_len), q, stream)
-    return _on_side(stream, _native.sparse_decode_q4(q, k_pool, v_pool, chunk_table, topk_idx, topk_count, window_start,
-                                                     window_len, max_window_len, dv, scale, k_scale, v_scale, out,
-                                                     out_dtype, lse, want_lse, status, ws, stream.cuda_stream))
+    if stream is not None:
+        return _on_stream(stream, _native.sparse_decode_q4, q, k_pool, v_pool, chunk_table, topk_idx, topk_count,
+                          window_start, window_len, max_window_len, dv, scale, k_scale, v_scale, out, out_dtype, lse,
+                          want_lse, status, ws, stream.cuda_stream)
+    return _native.sparse_decode_q4(q, k_pool, v_pool, chunk_table, topk_idx, topk_count, window_start, window_len,
+                                    max_window_len, dv, scale, k_scale, v_scale, out, out_dtype, lse, want_lse, status,
+                                    ws, None)
 
 
 # ------------------------------------------------------------------- a7 ----
@@ -576,6 +597,7 @@ def label_vote_workspace_size(n_layers, n_steps, n_chunks):
     return _lib.lsa_label_vote_workspace_size(n_layers, n_steps, n_chunks)
 
 
+@_ordered
 def label_vote(scores, top_p=0.6, min_layers=3, mode=0, *, ws=None, stream=None):
     """Cross-layer majority vote.  scores [layers, steps, chunks] fp32 -> (labels uint8, max_votes int32)."""
     _dev(scores, torch.float32, "scores")
