@@ -296,7 +296,7 @@ __global__ void __launch_bounds__(WARPS * 32, C::CTAS) q4_decode_kernel(const De
         amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
         amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
         float inv;
-        const float e = fmaxf(row_exponent(amax, inv) * p.scale_log2, 1.2e-38f);   // not 0: 0 * -inf is NaN
+        const float e = score_factor(row_exponent(amax, inv), p.scale_log2);
         smul[n][0] = __shfl_sync(0xffffffffu, e, 8 * t);        // head 2t: lane (2t, 0)
         smul[n][1] = __shfl_sync(0xffffffffu, e, 8 * t + 4);
 #pragma unroll
@@ -397,23 +397,23 @@ __global__ void __launch_bounds__(WARPS * 32, C::CTAS) q4_decode_kernel(const De
                     if (!((half >> (16 * (mt & 1) + g + 8)) & 1u)) s[mt][n][2] = s[mt][n][3] = -INFINITY;
                 }
             }
-            // the factor is positive: the maximum of the raw products is the scores'
+            // the factor is positive: the maximum of the raw products is the scores', and the reference is kept
+            // as a raw product (see score_factor)
             float mx0 = -INFINITY, mx1 = -INFINITY;
 #pragma unroll
             for (int mt = 0; mt < 4; ++mt) {
                 mx0 = fmaxf(mx0, fmaxf(s[mt][n][0], s[mt][n][2]));
                 mx1 = fmaxf(mx1, fmaxf(s[mt][n][1], s[mt][n][3]));
             }
-            mx0 *= smul[n][0];
-            mx1 *= smul[n][1];
 #pragma unroll
             for (int q = 4; q < 32; q *= 2) {
                 mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, q));
                 mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, q));
             }
-            const bool move0 = mx0 > m_ref[n][0] + RESCALE, move1 = mx1 > m_ref[n][1] + RESCALE;
+            const bool move0 = (mx0 - m_ref[n][0]) * smul[n][0] > RESCALE, move1 = (mx1 - m_ref[n][1]) * smul[n][1] > RESCALE;
             if (__any_sync(0xffffffffu, move0 || move1)) {
-                const float a0 = move0 ? ex2(m_ref[n][0] - mx0) : 1.f, a1 = move1 ? ex2(m_ref[n][1] - mx1) : 1.f;
+                const float a0 = move0 ? ex2((m_ref[n][0] - mx0) * smul[n][0]) : 1.f;
+                const float a1 = move1 ? ex2((m_ref[n][1] - mx1) * smul[n][1]) : 1.f;
                 if (move0) m_ref[n][0] = mx0;
                 if (move1) m_ref[n][1] = mx1;
                 l[n][0] *= a0;
@@ -424,12 +424,12 @@ __global__ void __launch_bounds__(WARPS * 32, C::CTAS) q4_decode_kernel(const De
                     o[j][n][2] *= a0; o[j][n][3] *= a1;
                 }
             }
-            const float r0 = m_ref[n][0] == -INFINITY ? 0.f : m_ref[n][0] - P_SHIFT;
-            const float r1 = m_ref[n][1] == -INFINITY ? 0.f : m_ref[n][1] - P_SHIFT;
+            const float r0 = m_ref[n][0] == -INFINITY ? 0.f : m_ref[n][0];
+            const float r1 = m_ref[n][1] == -INFINITY ? 0.f : m_ref[n][1];
 #pragma unroll
             for (int mt = 0; mt < 4; ++mt) {
-                const float p0 = ex2(fmaf(s[mt][n][0], smul[n][0], -r0)), p1 = ex2(fmaf(s[mt][n][1], smul[n][1], -r1));
-                const float p2 = ex2(fmaf(s[mt][n][2], smul[n][0], -r0)), p3 = ex2(fmaf(s[mt][n][3], smul[n][1], -r1));
+                const float p0 = ex2(fmaf(s[mt][n][0] - r0, smul[n][0], P_SHIFT)), p1 = ex2(fmaf(s[mt][n][1] - r1, smul[n][1], P_SHIFT));
+                const float p2 = ex2(fmaf(s[mt][n][2] - r0, smul[n][0], P_SHIFT)), p3 = ex2(fmaf(s[mt][n][3] - r1, smul[n][1], P_SHIFT));
                 l[n][0] += p0 + p2;
                 l[n][1] += p1 + p3;
                 pt[mt][n][0] = transpose8x8(pack_f16x2(p0, p1));
@@ -487,7 +487,7 @@ __global__ void __launch_bounds__(WARPS * 32, C::CTAS) q4_decode_kernel(const De
 #pragma unroll
             for (int q = 4; q < 32; q *= 2) x += __shfl_xor_sync(0xffffffffu, x, q);
             if (g == 0) {
-                sm_m[warp][8 * n + 2 * t + c] = m_ref[n][c] - P_SHIFT;
+                sm_m[warp][8 * n + 2 * t + c] = fmaf(m_ref[n][c], smul[n][c], -P_SHIFT);
                 sm_l[warp][8 * n + 2 * t + c] = x;
             }
         }

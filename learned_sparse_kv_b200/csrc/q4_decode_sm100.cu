@@ -316,7 +316,7 @@ __global__ void __launch_bounds__(THREADS, 1) q4_mla_kernel(const DecodeParams p
             amax = warp_max(amax);
             float inv;
             const float e = q4::row_exponent(amax, inv);
-            if (lane == 0) sm.qmul[h] = fmaxf(e * p.scale_log2, 1.2e-38f);   // not 0: 0 * -inf is NaN
+            if (lane == 0) sm.qmul[h] = q4::score_factor(e, p.scale_log2);
 #pragma unroll
             for (int i = 0; i < 3; ++i) {
                 const int piece = lane + 32 * i;
@@ -469,7 +469,7 @@ __global__ void __launch_bounds__(THREADS, 1) q4_mla_kernel(const DecodeParams p
             tc_fence_after();
             // Two passes over S (maximum, then weights), 32 columns at a time: 64 scores at once
             // would not fit the registers of 24 warps.  The factor is positive, so the
-            // maximum of the raw products is the scores'.
+            // maximum of the raw products is the scores', and m_ref is a raw product (see score_factor).
             uint32_t raw[32];
             auto fetch = [&](int q) {
                 tmem_ld32(tmem + lane_base + TM_S + 64 * s + 32 * q, raw);
@@ -487,13 +487,13 @@ __global__ void __launch_bounds__(THREADS, 1) q4_mla_kernel(const DecodeParams p
 #pragma unroll
                 for (int i = 0; i < 32; ++i) mx4[i & 3] = fmaxf(mx4[i & 3], __uint_as_float(raw[i]));
             }
-            float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * mul;
+            float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
             sm.red[u & 1][L] = mx;
             __syncwarp();
             named_barrier(1, 128);
             mx = fmaxf(mx, sm.red[u & 1][L ^ 64]);
-            const bool move = mx > m_ref + q4::RESCALE;
-            const float alpha = move ? ex2(m_ref - mx) : 1.f;      // 0 the first time (m_ref = -inf)
+            const bool move = (mx - m_ref) * mul > q4::RESCALE;
+            const float alpha = move ? ex2((m_ref - mx) * mul) : 1.f;      // 0 the first time (m_ref = -inf)
             if (move) {
                 l *= alpha;
                 m_ref = mx;
@@ -519,7 +519,7 @@ __global__ void __launch_bounds__(THREADS, 1) q4_mla_kernel(const DecodeParams p
                 tmem_wait_st();
                 tc_fence_before();
             }
-            const float ref = m_ref == -INFINITY ? 0.f : m_ref - q4::P_SHIFT;
+            const float ref = m_ref == -INFINITY ? 0.f : m_ref;
             // P V of tile u over the other unit needs this warp's lanes of O rescaled, though not its P, so
             // the warp arrives for that unit too -- once P V of tile u - 1 over it is done: only then has the
             // barrier's phase of tile u begun (the peer CTA may be a tile behind).
@@ -540,8 +540,8 @@ __global__ void __launch_bounds__(THREADS, 1) q4_mla_kernel(const DecodeParams p
                 uint32_t pk[16];
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
-                    const float p0 = ex2(fmaf(__uint_as_float(raw[2 * i]), mul, -ref));
-                    const float p1 = ex2(fmaf(__uint_as_float(raw[2 * i + 1]), mul, -ref));
+                    const float p0 = ex2(fmaf(__uint_as_float(raw[2 * i]) - ref, mul, q4::P_SHIFT));
+                    const float p1 = ex2(fmaf(__uint_as_float(raw[2 * i + 1]) - ref, mul, q4::P_SHIFT));
                     psum[i & 3] += p0 + p1;
                     pk[i] = q4::pack_f16x2(p0, p1);
                 }
@@ -577,7 +577,7 @@ __global__ void __launch_bounds__(THREADS, 1) q4_mla_kernel(const DecodeParams p
         const int head = HPC * (int)rank + h;
         const size_t part0 = ((size_t)b * p.n_splits + split) * p.Hq;
         if (half == 0 && head < p.Hq) {
-            p.m_part[part0 + head] = m_ref - q4::P_SHIFT;
+            p.m_part[part0 + head] = n_tiles > 0 ? fmaf(m_ref, mul, -q4::P_SHIFT) : -INFINITY;
             p.l_part[part0 + head] = l_tot;
         }
     }

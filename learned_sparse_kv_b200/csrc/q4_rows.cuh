@@ -90,6 +90,12 @@ __device__ __forceinline__ float row_exponent(float amax, float &inv) {
     return __uint_as_float(e << 23);
 }
 
+// Factor from raw products to scores in base 2.  Positive, so that it keeps the order, and finite: 0 * inf is NaN.
+// References are raw products and weights exp2((s - m_ref) * factor + P_SHIFT): the difference is 0 at the
+// reference however large the scores are.  With the factor applied first, the roundings of two products of 2^29
+// (half a step is 16 there) would push the largest weight out of f16's range, or to zero.
+__device__ __forceinline__ float score_factor(float e, float scale_log2) { return fminf(fmaxf(e * scale_log2, 1.2e-38f), 3e38f); }
+
 }  // namespace q4
 
 namespace q4mla {

@@ -1,0 +1,54 @@
+"""Attention over 4-bit pools at the ends of its ranges: scores of any size, queries with an entry far above the others,
+weights that a caller of fp32 output can rely on."""
+import numpy as np
+import pytest
+import torch
+
+from tests import q4_reference as R
+from tests.test_gpu_q4 import _case, _run, status
+
+pytestmark = pytest.mark.gpu
+CH = 64
+SHAPES = [(8, 1, 128, 128, False), (16, 1, 128, 128, False), (12, 1, 64, 64, False), (128, 1, 576, 512, True)]
+
+
+@pytest.fixture(scope="module")
+def L():
+    from learned_sparse_kv_b200 import lsa
+    return lsa
+
+
+def _one_column(c, column, top, q):
+    """Key column `column` holds 6 at position `top` and 0.5 .. 4 elsewhere, in scales of one; queries are 0 but there."""
+    codes, scales = (a.copy() for a in R.unpack(c["kp"]))
+    group = slice(column // 16 * 16, column // 16 * 16 + 16)
+    codes[..., group] = 0
+    codes[..., column] = np.random.default_rng(1).integers(1, 7, codes.shape[:-1])
+    scales[..., column // 16] = 0x38
+    codes[c["table"][0, top // CH], :, top % CH, column] = 7
+    c["kp"][...] = R.pack(codes, scales)
+    c["q"] = torch.zeros_like(c["q"])
+    c["q"][0, :, column] = q
+
+
+@pytest.mark.parametrize("Hq,heads,dqk,dv,latent", SHAPES)
+@pytest.mark.parametrize("n,top", [(300, 130), (3000, 2999), (64, 0)])
+def test_scores_of_any_size(L, Hq, heads, dqk, dv, latent, n, top):
+    """Scores of 2^9 to 2^100: one row has the largest by a third, so the output is its value row, exactly (a weight of a
+    power of two over itself), and the lse is its score, whatever the roundings of the other scores are."""
+    rng = np.random.default_rng(n)
+    for lo, hi in ((9, 21), (21, 27), (27, 31), (31, 36), (36, 100)):
+        c = _case(3, 1, Hq, heads, dqk, dv, latent, 0, [0], [n])
+        mult = rng.integers(128, 256, Hq) / 128.0 * 2.0 ** rng.integers(lo, hi, Hq)
+        _one_column(c, 3 if not latent else 560, top, torch.from_numpy(mult).bfloat16())
+        c["scale"] = 1.0 / 6.0
+        st = status()
+        out, lse = _run(L, c, torch.float32, st=st)
+        assert st.item() == 0
+        vv = R.pool_values(c["kp"] if latent else c["vp"])[..., :dv]
+        want = vv[c["table"][0, top // CH], 0, top % CH]
+        got = out[0].double().cpu().numpy()
+        wrong = [(h, got[h, 0], want[0]) for h in np.flatnonzero((got != want).any(-1))]
+        assert not wrong, (lo, hi, len(wrong), wrong[:4])
+        score = c["q"][0].double().numpy().max(-1)
+        assert np.all(np.abs(lse[0].double().cpu().numpy() - score) <= 2.0 ** -21 * score)
