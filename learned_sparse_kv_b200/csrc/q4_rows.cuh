@@ -80,14 +80,14 @@ struct Units {
 // error of 2^-12 on each weight, an eighth of what rounding a bf16 result leaves.
 constexpr float RESCALE = 8.f, P_SHIFT = 6.f;
 
-// Queries enter Q K^T as f16 after a division by a power of two that brings the largest entry
-// of the row into [1, 2): bf16 has fewer significant bits than f16, so entries down to 2^-16 of the
-// largest are exact and the rest are off by at most 2^-25 of it.
+// Queries enter Q K^T as f16 after a multiplication by a power of two that brings the largest entry of the row into
+// [2^15, 2^16), the top of f16's range: f16 queries lose nothing, bf16 ones, which have fewer significant bits, are
+// exact down to 2^-32 of the largest, and what is smaller is off by at most 2^-40 of it.
+// Products of up to 2^16 * 2688 and their sums are fp32.  Rows below 2^-111 are brought as far up as fp32 factors go.
 __device__ __forceinline__ float row_exponent(float amax, float &inv) {
-    const uint32_t e = (__float_as_uint(amax) >> 23) & 255u;
-    if (e == 0u || e >= 254u) { inv = 1.f; return 1.f; }   // zero, subnormal, infinite or NaN
-    inv = __uint_as_float((254u - e) << 23);
-    return __uint_as_float(e << 23);
+    const uint32_t e = max((__float_as_uint(amax) >> 23) & 255u, 16u);     // 255, infinite or NaN: stays so
+    inv = __uint_as_float((269u - e) << 23);
+    return __uint_as_float((e - 15u) << 23);
 }
 
 // Factor from raw products to scores in base 2.  Positive, so that it keeps the order, and finite: 0 * inf is NaN.

@@ -52,3 +52,31 @@ def test_scores_of_any_size(L, Hq, heads, dqk, dv, latent, n, top):
         assert not wrong, (lo, hi, len(wrong), wrong[:4])
         score = c["q"][0].double().numpy().max(-1)
         assert np.all(np.abs(lse[0].double().cpu().numpy() - score) <= 2.0 ** -21 * score)
+
+
+@pytest.mark.parametrize("Hq,heads,dqk,dv,latent", SHAPES)
+@pytest.mark.parametrize("dtype,power", [(torch.bfloat16, 20), (torch.bfloat16, 30), (torch.float16, 15)])
+def test_queries_with_one_large_entry(L, Hq, heads, dqk, dv, latent, dtype, power):
+    """One query entry of 2^power beside ordinary ones of 1/4 and more, over a key column of zeros: what is left of the
+    scores is the ordinary entries', whose f16 images are exact (2^-32 of the largest or more).  So the bounds are
+    those of test_gpu_q4 without its term for query entries below f16's range."""
+    c = _case(17, 2, Hq, heads, dqk, dv, latent, 70, [128, 100], [300, 65], dtype=torch.float32)
+    column = 5
+    codes, scales = (a.copy() for a in R.unpack(c["kp"]))
+    codes[..., column] &= 8
+    c["kp"][...] = R.pack(codes, scales)
+    q = c["q"]
+    q = torch.sign(q) * q.abs().clamp(min=0.25)
+    q[..., column] = 2.0 ** power
+    c["q"] = q.to(dtype)
+    out, lse = _run(L, c, torch.float32)
+    kv = R.pool_values(c["kp"])
+    vv = None if latent else R.pool_values(c["vp"])
+    o, s = out.double().cpu().numpy(), lse.double().cpu().numpy()
+    for b in range(2):
+        rows = R.row_set(b, c["table"], c["topk"], c["count"], c["start"], c["length"], len(c["kp"]))
+        ro, rl, spread, mag, flat = R.attend(c["q"][b].double().numpy(), kv, vv, dv, rows, c["scale"])
+        D = (dqk + 32) * 2.0 ** -23 * mag
+        tol = (2.0 ** -11 + 2 * D[:, None] + 2.0 ** -20 + len(rows) * 2.0 ** -24) * spread + 2.0 ** -24 * np.abs(ro) + 2.0 ** -31 * flat
+        assert np.all(np.abs(o[b] - ro) <= tol), (b, float((np.abs(o[b] - ro) / tol).max()))
+        assert np.all(np.abs(s[b] - rl) <= D + 2.0 ** -20 + 2.0 ** -22 * np.abs(rl)), b
