@@ -548,8 +548,8 @@ int lsa_read_q4(const uint8_t *pool, int64_t n_slots, int heads, int width, floa
  * sequence without rows gives out = 0, lse = -inf.
  *   q [B, Hq, dqk] bf16 or f16; out [B, Hq, dv] bf16, f16 or fp32; lse [B, Hq] fp32 (optional)
  *   max_window_len: host upper bound of window_len[b]; it sizes the split-K grid only
- * Softmax weights enter the value product as f16 (11 significant bits); scores, sums and
- * outputs accumulate in fp32.
+ * Softmax weights enter the value product as f16 for a bf16 result (11 significant bits), and as two f16
+ * parts (22 bits) for an f16 or fp32 result; scores, sums and outputs accumulate in fp32.
  * dev_status: LSA_DEV_TABLE (a needed chunk has no valid slot, or the window is longer than its table
  * row: its rows are skipped), LSA_DEV_INDEX (a negative position: skipped; a negative window_start: no
  * window), LSA_DEV_TIMEOUT.

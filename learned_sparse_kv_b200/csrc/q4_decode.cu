@@ -146,7 +146,7 @@ __device__ __forceinline__ float lse_of(float M, float L) {
     return L == 0.f ? -INFINITY : (M + log2f(L)) * 0.69314718055994530942f;
 }
 
-template <class C>
+template <class C, bool TWO>
 __global__ void __launch_bounds__(WARPS * 32, C::CTAS) q4_decode_kernel(const DecodeParams p, int B) {
     constexpr int D = C::D, NH = C::NH, NT = WARPS * 32;
     extern __shared__ __align__(128) uint8_t smem[];
@@ -386,7 +386,7 @@ __global__ void __launch_bounds__(WARPS * 32, C::CTAS) q4_decode_kernel(const De
         }
 
         // ---- softmax over the unit's rows; a head's column lives in the 8 lanes of equal t
-        uint32_t pt[4][NH][2];
+        uint32_t pt[4][NH][2], pl[4][NH][TWO ? 2 : 1];
 #pragma unroll
         for (int n = 0; n < NH; ++n) {
             if (!full) {
@@ -432,8 +432,13 @@ __global__ void __launch_bounds__(WARPS * 32, C::CTAS) q4_decode_kernel(const De
                 const float p2 = ex2(fmaf(s[mt][n][2] - r0, smul[n][0], P_SHIFT)), p3 = ex2(fmaf(s[mt][n][3] - r1, smul[n][1], P_SHIFT));
                 l[n][0] += p0 + p2;
                 l[n][1] += p1 + p3;
-                pt[mt][n][0] = transpose8x8(pack_f16x2(p0, p1));
-                pt[mt][n][1] = transpose8x8(pack_f16x2(p2, p3));
+                const uint32_t h0 = pack_f16x2(p0, p1), h1 = pack_f16x2(p2, p3);
+                pt[mt][n][0] = transpose8x8(h0);
+                pt[mt][n][1] = transpose8x8(h1);
+                if constexpr (TWO) {
+                    pl[mt][n][0] = transpose8x8(rest_f16x2(p0, p1, h0));
+                    pl[mt][n][1] = transpose8x8(rest_f16x2(p2, p3, h1));
+                }
             }
         }
 
@@ -469,7 +474,10 @@ __global__ void __launch_bounds__(WARPS * 32, C::CTAS) q4_decode_kernel(const De
                     const uint32_t a0 = hmul2(e01[j], s01), a1 = hmul2(o01[j], s01);
                     const uint32_t a2 = hmul2(e23[j], s23), a3 = hmul2(o23[j], s23);
 #pragma unroll
-                    for (int n = 0; n < NH; ++n) mma_f16(o[4 * w + j][n], a0, a1, a2, a3, pt[mt][n][0], pt[mt][n][1]);
+                    for (int n = 0; n < NH; ++n) {
+                        mma_f16(o[4 * w + j][n], a0, a1, a2, a3, pt[mt][n][0], pt[mt][n][1]);
+                        if constexpr (TWO) mma_f16(o[4 * w + j][n], a0, a1, a2, a3, pl[mt][n][0], pl[mt][n][1]);
+                    }
                 }
             }
         }
@@ -684,11 +692,11 @@ static int separate_ctas(int B, int heads, int G, int units) {
     return (int)lsa_max64(1, lsa_min64(sm_count() * (G <= 8 ? 3 : 2), most));
 }
 
-template <class C>
+template <class C, bool TWO>
 static int launch_separate(const DecodeParams &p, int B, cudaStream_t stream) {
     static std::atomic<uint64_t> done{0};
-    if (int rc = allow_shared(q4_decode_kernel<C>, C::SMEM, done)) return rc;
-    q4_decode_kernel<C><<<p.n_splits, WARPS * 32, C::SMEM, stream>>>(p, B);
+    if (int rc = allow_shared(q4_decode_kernel<C, TWO>, C::SMEM, done)) return rc;
+    q4_decode_kernel<C, TWO><<<p.n_splits, WARPS * 32, C::SMEM, stream>>>(p, B);
     if (int rc = check_launch("q4_decode_kernel")) return rc;
     q4_merge_split_kernel<C::D, C::HPC><<<dim3(p.Hq, B), MERGE, 0, stream>>>(p);
     return check_launch("q4_merge_split_kernel");
@@ -779,7 +787,9 @@ extern "C" int lsa_sparse_decode_q4(int q_dtype, const void *q, const uint8_t *k
         q4::q4_merge_kernel<<<dim3(Hq, B), dv / 4, 0, stream>>>(p, dv);
         return check_launch("q4_merge_kernel");
     }
-    if (dqk == 128)
-        return G <= 8 ? q4::launch_separate<q4::Cfg<128, 1>>(p, B, stream) : q4::launch_separate<q4::Cfg<128, 2>>(p, B, stream);
-    return G <= 8 ? q4::launch_separate<q4::Cfg<64, 1>>(p, B, stream) : q4::launch_separate<q4::Cfg<64, 2>>(p, B, stream);
+    const bool two = q4::two_parts(out_dtype);
+#define LSA_SEPARATE(D, NH) (two ? q4::launch_separate<q4::Cfg<D, NH>, true>(p, B, stream) : q4::launch_separate<q4::Cfg<D, NH>, false>(p, B, stream))
+    if (dqk == 128) return G <= 8 ? LSA_SEPARATE(128, 1) : LSA_SEPARATE(128, 2);
+    return G <= 8 ? LSA_SEPARATE(64, 1) : LSA_SEPARATE(64, 2);
+#undef LSA_SEPARATE
 }

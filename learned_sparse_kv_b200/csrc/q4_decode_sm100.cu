@@ -66,6 +66,8 @@ struct __align__(1024) Smem {
     uint64_t k_empty[KG];               // the MMAs that read that part of K are done
     uint64_t pv_full[2];                // the even CTA's, 16 arrivals: V and P of unit a of the tile are written
     uint64_t pv_done[2];                // P V over unit a is done: its V and P may be rewritten
+    uint64_t first_done[2];             // two-part weights: the product with the first part is done, P may be rewritten
+    uint64_t rest_full[2];              // the even CTA's, 4 arrivals: the second part of P of unit a is written
     uint64_t s_full[2];                 // S buffers
     uint64_t info_full[INFO];
     uint64_t mma_done;                  // all MMAs are done
@@ -202,6 +204,9 @@ struct RowPtr {
     }
 };
 
+// TWO: weights in two parts (q4::two_parts).  The second goes through the same P buffer once the first has been
+// multiplied, so a tile's products take 1300 cycles more.
+template <bool TWO>
 __global__ void __launch_bounds__(THREADS, 1) q4_mla_kernel(const DecodeParams p, int stall) {
     extern __shared__ uint8_t smem_raw[];
     Smem &sm = *reinterpret_cast<Smem *>(smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023));
@@ -219,6 +224,8 @@ __global__ void __launch_bounds__(THREADS, 1) q4_mla_kernel(const DecodeParams p
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sm.pv_full[i], DEQ + 8);
             mbar_init(&sm.pv_done[i], 1);
+            mbar_init(&sm.first_done[i], 1);
+            mbar_init(&sm.rest_full[i], 4);
             mbar_init(&sm.s_full[i], 1);
         }
         for (int i = 0; i < INFO; ++i) mbar_init(&sm.info_full[i], DEQ);
@@ -349,7 +356,8 @@ __global__ void __launch_bounds__(THREADS, 1) q4_mla_kernel(const DecodeParams p
         if (stall) ok = warp_wait(sm, &sm.never, 0, p.status, STALL_CYCLES);
 #pragma unroll 1
         for (int u = -1; u < n_tiles && ok; ++u) {
-            // The S buffer of tile u + 1 was read before P of tile u - 1 was written, which P V(u - 1) waited for.
+            // The S buffer of tile u + 1 was read before P of tile u - 1 (all of its parts) was written, which
+            // P V(u - 1) waited for.
             const int n = u + 1, sb = n & 1;
             if (n < n_tiles) {
                 ok = warp_wait(sm, &sm.k_full, n & 1, p.status);
@@ -372,8 +380,9 @@ __global__ void __launch_bounds__(THREADS, 1) q4_mla_kernel(const DecodeParams p
                 __syncwarp();
             }
 #pragma unroll 1
-            for (int a = 0; a < 2 && u >= 0; ++a) {
-                ok = warp_wait(sm, &sm.pv_full[a], u & 1, p.status);
+            for (int i = 0; i < (TWO ? 4 : 2) && u >= 0; ++i) {
+                const int a = i & 1;
+                ok = warp_wait(sm, i < 2 ? &sm.pv_full[a] : &sm.rest_full[a], u & 1, p.status);
                 if (!ok) break;
                 tc_fence_after();
                 if (elect_one()) {
@@ -382,8 +391,8 @@ __global__ void __launch_bounds__(THREADS, 1) q4_mla_kernel(const DecodeParams p
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk)
                             umma_pair_ss(tmem + TM_O + 128 * j, pd + P_ATOM * a + K16 * kk, vd + V_J * j + V16 * (4 * a + kk), IDESC_PV,
-                                         (u | a | kk) != 0);
-                    umma_commit_pair(&sm.pv_done[a], 0x3);
+                                         (u | i | kk) != 0);
+                    umma_commit_pair(!TWO || i >= 2 ? &sm.pv_done[a] : &sm.first_done[a], 0x3);
                 }
                 __syncwarp();
             }
@@ -560,6 +569,33 @@ __global__ void __launch_bounds__(THREADS, 1) q4_mla_kernel(const DecodeParams p
             __syncwarp();
             if (lane == 0) mbar_arrive_cluster(map_to_rank(&sm.pv_full[half], 0));
             if (half == 0) turn(1);
+            if constexpr (TWO) {
+                // the second part, from the same S (its buffer is written again after P V of this tile)
+#pragma unroll 1
+                for (int q = 0; q < 2; ++q) {
+                    fetch(q);
+                    uint32_t pk[16];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const float p0 = ex2(fmaf(__uint_as_float(raw[2 * i]) - ref, mul, q4::P_SHIFT));
+                        const float p1 = ex2(fmaf(__uint_as_float(raw[2 * i + 1]) - ref, mul, q4::P_SHIFT));
+                        pk[i] = q4::rest_f16x2(p0, p1, q4::pack_f16x2(p0, p1));
+                    }
+                    if (q == 0) {
+                        if (ok) ok = wait_for(&sm.first_done[half], u & 1, &sm.abort_flag);
+                        if (!ok && *(volatile int *)&sm.abort_flag == 0) set_abort(sm, p.status);
+                    }
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        *reinterpret_cast<uint4 *>(prow + (((4 * q + c) ^ (h & 7)) << 4)) =
+                            make_uint4(pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
+                    __syncwarp();
+                }
+                tc_fence_before();
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(map_to_rank(&sm.rest_full[half], 0));
+            }
         }
         // ---- epilogue: wait for the last P V, then write the partial
 #pragma unroll 1
@@ -644,10 +680,11 @@ int splits(int B, int max_units) {
     return max(1, min(min(clusters / max(B, 1), clusters / 2), tiles));
 }
 
-int launch(const DecodeParams &p, int B, cudaStream_t stream) {
+template <bool TWO>
+static int launch_parts(const DecodeParams &p, int B, cudaStream_t stream) {
     const size_t smem = sizeof(Smem) + 1024;
     static std::atomic<uint64_t> done{0};
-    if (int rc = allow_shared(q4_mla_kernel, (int)smem, done)) return rc;
+    if (int rc = allow_shared(q4_mla_kernel<TWO>, (int)smem, done)) return rc;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2 * p.n_splits, B, 1);
     cfg.blockDim = dim3(THREADS, 1, 1);
@@ -660,8 +697,11 @@ int launch(const DecodeParams &p, int B, cudaStream_t stream) {
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    LSA_CUDA(cudaLaunchKernelEx(&cfg, q4_mla_kernel, p, take_test_stall(LSA_TEST_STALL_ATTENTION_Q4)));
+    LSA_CUDA(cudaLaunchKernelEx(&cfg, q4_mla_kernel<TWO>, p, take_test_stall(LSA_TEST_STALL_ATTENTION_Q4)));
     return LSA_OK;
+}
+int launch(const DecodeParams &p, int B, cudaStream_t stream) {
+    return q4::two_parts(p.out_dtype) ? launch_parts<true>(p, B, stream) : launch_parts<false>(p, B, stream);
 }
 
 }  // namespace q4mla

@@ -77,8 +77,20 @@ struct Units {
 // the row maximum only when that has grown by more than 2^RESCALE (so O is rarely rescaled).
 // The largest weight is 2^(P_SHIFT + RESCALE) = 2^14 < 65504; a weight stays a normal f16
 // number, 11 significant bits, down to 2^-20 of the largest.  Rounding it so leaves a relative
-// error of 2^-12 on each weight, an eighth of what rounding a bf16 result leaves.
+// error of 2^-12 on each weight, an eighth of what rounding a bf16 result leaves, so one part
+// serves bf16 outputs.  For f16 and fp32 outputs it would be the largest error of all; there a weight has two
+// parts, its f16 rounding and the f16 rounding of the rest, 22 significant bits, and the value product is done
+// for both.  Measured, two parts and one: 512K rows whole 71.0 and 64.4 us, 16 ragged sequences 20.2 and 18.9,
+// latent rows 49.5 and 38.8 (8 x 10K rows, 128 heads), 169 and 122.6 (32 x 10K, 64 heads); the error of an f16 result
+// against 64 bits is 1.0 and 1.4 times that of its rounding alone.
 constexpr float RESCALE = 8.f, P_SHIFT = 6.f;
+inline bool two_parts(int out_dtype) { return out_dtype != LSA_DTYPE_BF16; }
+
+// What an f16 pair of weights leaves of them.
+__device__ __forceinline__ uint32_t rest_f16x2(float lo, float hi, uint32_t rounded) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&rounded));
+    return pack_f16x2(lo - f.x, hi - f.y);
+}
 
 // Queries enter Q K^T as f16 after a multiplication by a power of two that brings the largest entry of the row into
 // [2^15, 2^16), the top of f16's range: f16 queries lose nothing, bf16 ones, which have fewer significant bits, are

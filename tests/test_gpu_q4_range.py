@@ -80,3 +80,26 @@ def test_queries_with_one_large_entry(L, Hq, heads, dqk, dv, latent, dtype, powe
         tol = (2.0 ** -11 + 2 * D[:, None] + 2.0 ** -20 + len(rows) * 2.0 ** -24) * spread + 2.0 ** -24 * np.abs(ro) + 2.0 ** -31 * flat
         assert np.all(np.abs(o[b] - ro) <= tol), (b, float((np.abs(o[b] - ro) / tol).max()))
         assert np.all(np.abs(s[b] - rl) <= D + 2.0 ** -20 + 2.0 ** -22 * np.abs(rl)), b
+
+
+@pytest.mark.parametrize("Hq,heads,dqk,dv,latent", SHAPES)
+@pytest.mark.parametrize("out_dtype", [torch.float32, torch.float16])
+@pytest.mark.parametrize("n", [2, 17, 67, 200])
+def test_weights_of_f16_and_fp32_outputs(L, Hq, heads, dqk, dv, latent, out_dtype, n):
+    """Scores that are exact products (one key column, one query entry) leave the weights' own error: 2^-22 for the two
+    parts, 2^-20 for the exponential and its argument, n 2^-24 for the sums, of sum_j p_j |v_j|; 2^-31 of the largest
+    weight where a weight is below f16's normal range (see test_gpu_q4); and the rounding of the result."""
+    rng = np.random.default_rng(n)
+    c = _case(23, 1, Hq, heads, dqk, dv, latent, 0, [0], [n])
+    _one_column(c, 3 if not latent else 560, n // 2, torch.from_numpy(rng.uniform(0.1, 1.5, Hq)).bfloat16())
+    c["scale"] = 0.25
+    out, lse = _run(L, c, out_dtype)
+    kv = R.pool_values(c["kp"])
+    vv = None if latent else R.pool_values(c["vp"])
+    rows = R.row_set(0, c["table"], c["topk"], c["count"], c["start"], c["length"], len(c["kp"]))
+    ro, rl, spread, _, flat = R.attend(c["q"][0].double().numpy(), kv, vv, dv, rows, c["scale"])
+    tol = (2.0 ** -22 + 2.0 ** -20 + n * 2.0 ** -24) * spread + torch.finfo(out_dtype).eps / 2 * np.abs(ro) + 2.0 ** -31 * flat
+    tol += 2.0 ** -25 * (out_dtype == torch.float16)            # half a step of f16's subnormals
+    off = np.abs(out[0].double().cpu().numpy() - ro) / tol.clip(1e-300)
+    assert off.max() <= 1, (float(off.max()), int((off > 1).sum()))
+    assert np.all(np.abs(lse[0].double().cpu().numpy() - rl) <= 2.0 ** -20 + 2.0 ** -22 * np.abs(rl))
