@@ -31,8 +31,9 @@
 // chains does not help: eight softmax warps of 32 columns a thread 41.2 us, rows looked up by one warp for
 // all 40.0, loads of a row by 12 neighbouring lanes 42.9.  A launch spends 9,000 cycles on its prologue
 // (lengths, positions, slots, codes: loads that wait for each other).
-// Every mbarrier wait is bounded: on timeout the kernel sets LSA_DEV_TIMEOUT and the abort flag of
-// both CTAs, the other waits return, the MMAs issued so far complete, and the pair exits.  No
+// Every mbarrier wait is bounded, each by itself and never the launch as a whole: on timeout the kernel sets
+// LSA_DEV_TIMEOUT and the abort flag of both CTAs, the other waits return, the MMAs issued so far complete (a wait
+// that starts when all roles have ended and that the abort flag does not cut short), and the pair exits.  No
 // copy is asynchronous (codes come through registers), so nothing else is in flight.
 #include "q4_rows.cuh"
 #include "sm100.cuh"
@@ -88,14 +89,14 @@ __device__ __noinline__ void set_abort(Smem &sm, int32_t *status) {
 }
 
 // Bounded wait on the SM's own clock: reading the global timer between two tries takes longer than most
-// of these waits last.  The limit is some two seconds of cycles; the abort flag is looked at after 2^18.
+// of these waits last.  The limit is some two seconds of cycles; the abort flag, if given, is looked at after 2^18.
 constexpr long long WAIT_CYCLES = 1ll << 32, STALL_CYCLES = 1ll << 22, ABORT_CYCLES = 1ll << 18;
 __device__ __noinline__ bool wait_longer(uint32_t a, uint32_t parity, const volatile int *abort, long long limit) {
     const long long t0 = clock64();
     for (;;) {
         if (mbar_try_wait(a, parity)) return true;
         const long long dt = clock64() - t0;
-        if (dt > limit || (dt > ABORT_CYCLES && *abort)) return false;
+        if (dt > limit || (abort && dt > ABORT_CYCLES && *abort)) return false;
     }
 }
 __device__ __forceinline__ bool wait_for(const uint64_t *bar, uint32_t parity, const volatile int *abort,
@@ -660,12 +661,12 @@ __global__ void __launch_bounds__(THREADS, 1) q4_mla_kernel(const DecodeParams p
     }
 
     // ---- teardown: every MMA finished before TMEM is released and before either CTA leaves
-    if (warp == 2 && n_tiles > 0) {
-        if (lane == 0 && !mbar_wait(&sm.mma_done, 0, WAIT_NS)) set_abort(sm, p.status);
-        __syncwarp();
-    }
     __syncwarp();
     __syncthreads();
+    if (warp == 2 && n_tiles > 0) {
+        if (lane == 0 && !wait_for(&sm.mma_done, 0, nullptr)) set_abort(sm, p.status);
+        __syncwarp();
+    }
     cluster_sync();
     if (warp == 2) {
         tc_fence_after();

@@ -103,3 +103,27 @@ def test_weights_of_f16_and_fp32_outputs(L, Hq, heads, dqk, dv, latent, out_dtyp
     off = np.abs(out[0].double().cpu().numpy() - ro) / tol.clip(1e-300)
     assert off.max() <= 1, (float(off.max()), int((off > 1).sum()))
     assert np.all(np.abs(lse[0].double().cpu().numpy() - rl) <= 2.0 ** -20 + 2.0 ** -22 * np.abs(rl))
+
+
+def test_a_launch_longer_than_any_wait(L):
+    """Latent rows of one sequence for some two seconds, on one pair of CTAs beside 37 short ones: a launch may last longer
+    than the bound of a single wait, and no wait runs out.  The table names one chunk over and over: every row counts
+    2^21 times, so the output is that of the chunk alone and its lse is larger by 21 log 2 (fp32 sums of 2^20 terms, each
+    off by at most 2^-24 of the sum: 2^-4)."""
+    n_ch, B = 2 ** 21, 38
+    rng = np.random.default_rng(4)
+    rows = torch.from_numpy(rng.standard_normal((CH, 1, 576))).to("cuda", torch.bfloat16)
+    pool = L.q4_pool(1, 1, 576)
+    L.write_q4(rows, pool, torch.arange(CH, device="cuda"))
+    q = torch.from_numpy(rng.standard_normal((1, 16, 576))).to("cuda", torch.bfloat16).repeat(B, 1, 1)
+    table = torch.zeros(B, n_ch, dtype=torch.int32, device="cuda")
+    start = torch.zeros(B, dtype=torch.int32, device="cuda")
+    length = torch.full((B,), CH, dtype=torch.int32, device="cuda")
+    length[0] = n_ch * CH
+    st = status()
+    out, lse = L.sparse_decode_q4(q, pool, None, table, None, None, start, length, n_ch * CH, 512, 0.04, status=st)
+    torch.cuda.synchronize()
+    assert st.item() == 0
+    assert torch.equal(out[1:], out[1:2].expand(B - 1, -1, -1))
+    assert float((lse[0] - lse[1] - 21 * np.log(2)).abs().max()) <= 2.0 ** -4
+    assert bool(torch.isfinite(out[0]).all())
