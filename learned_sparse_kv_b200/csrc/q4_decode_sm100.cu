@@ -516,6 +516,7 @@ __global__ void __launch_bounds__(THREADS, 1) q4_mla_kernel(const DecodeParams p
                     ok = ok && wait_for(&sm.pv_done[a], (u - 1) & 1, &sm.abort_flag);
                     if (!ok && *(volatile int *)&sm.abort_flag == 0) set_abort(sm, p.status);
                 }
+                __syncwarp();          // lanes wait for themselves; what follows takes converged warps
                 tc_fence_after();
 #pragma unroll 1
                 for (int q = 0; q < 8; ++q) {
@@ -536,6 +537,7 @@ __global__ void __launch_bounds__(THREADS, 1) q4_mla_kernel(const DecodeParams p
             auto done = [&](int a) {
                 if (ok) ok = wait_for(&sm.pv_done[a], (u - 1) & 1, &sm.abort_flag);
                 if (!ok && *(volatile int *)&sm.abort_flag == 0) set_abort(sm, p.status);
+                __syncwarp();          // the next columns are fetched by a converged warp
             };
             auto turn = [&](int a) {
                 if (u > 0) done(a);
@@ -585,12 +587,12 @@ __global__ void __launch_bounds__(THREADS, 1) q4_mla_kernel(const DecodeParams p
                     if (q == 0) {
                         if (ok) ok = wait_for(&sm.first_done[half], u & 1, &sm.abort_flag);
                         if (!ok && *(volatile int *)&sm.abort_flag == 0) set_abort(sm, p.status);
+                        __syncwarp();
                     }
 #pragma unroll
                     for (int c = 0; c < 4; ++c)
                         *reinterpret_cast<uint4 *>(prow + (((4 * q + c) ^ (h & 7)) << 4)) =
                             make_uint4(pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
-                    __syncwarp();
                 }
                 tc_fence_before();
                 fence_proxy_async_smem();
