@@ -74,6 +74,8 @@ class Window:
         """selector: None for the memory-indexer gate (OR mode when t has "nmi_union"), or a
         baseline: dict(mode=lsa.SELECT_RECENT) or dict(mode=lsa.SELECT_RANDOM, seed=.., keep_num=1,
         keep_den=10)."""
+        if cold and (t["kv"] if shapes.latent else t["k"]).dtype == torch.uint8:
+            raise lsa.LSAError(2, "4-bit pools are hot only: a cold window's pools are bf16")
         self.s = shapes
         self.selector = selector
         self.t = t
@@ -109,7 +111,6 @@ class Window:
         self.v_pool = None if shapes.latent else t["v"]
         self.q4 = self.k_pool.dtype == torch.uint8
         if self.q4:
-            assert not cold, "4-bit pools are hot"
             self.q4_scales = dict(k_scale=float(t.get("k_scale", 1.0)), v_scale=float(t.get("v_scale", 1.0)))
             dec_ws = lsa.sparse_decode_q4_workspace_size(B, shapes.Hq, self.k_pool.shape[1], shapes.dqk, shapes.dv,
                                                          shapes.k, self.max_window_len)
