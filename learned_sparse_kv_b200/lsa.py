@@ -496,7 +496,16 @@ def _load_binding():
     return module
 
 
-_native = _load_binding()
+class _Binding:
+    """Stands for the binding until its first call; the other calls do without it."""
+
+    def __getattr__(self, name):
+        global _native
+        _native = _load_binding()
+        return getattr(_native, name)
+
+
+_native = _Binding()
 
 
 def build_tables_workspace_size(B, table_stride, n_slots):
