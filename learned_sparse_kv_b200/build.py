@@ -16,6 +16,7 @@ CSRC = os.path.join(HERE, "csrc")
 OBJ = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "liblsa.so")
 BINDING = os.path.join(HERE, "_binding.so")
+STAMP = os.path.join(OBJ, "binding.torch")      # the torch and Python that the binding was built for
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
@@ -33,6 +34,30 @@ def _deps():
 
 def _torch_dir():
     return os.path.dirname(importlib.util.find_spec("torch").origin)
+
+
+def _torch_version():
+    with open(os.path.join(_torch_dir(), "version.py")) as f:
+        return f"{sys.version}\n{f.read()}"
+
+
+def _note_torch():
+    with open(STAMP, "w") as f:
+        f.write(_torch_version())
+
+
+def _binding_fits():
+    """Is the binding there, and built for this torch?"""
+    try:
+        with open(STAMP) as f:
+            return os.path.exists(BINDING) and f.read() == _torch_version()
+    except OSError:
+        return False
+
+
+def _build_binding():
+    _link_binding(_compile_binding())
+    _note_torch()
 
 
 def _compile_binding():
@@ -75,6 +100,9 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if not force and os.path.exists(LIB) and os.path.exists(BINDING):
         t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
         if all(os.path.getmtime(p) <= t for p in _deps()):
+            if not _binding_fits():
+                os.makedirs(OBJ, exist_ok=True)
+                _build_binding()
             return LIB
     os.makedirs(OBJ, exist_ok=True)
     srcs = _sources()
@@ -92,6 +120,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
         raise RuntimeError(f"link failed:\n{r.stderr}")
     os.replace(tmp, LIB)
     _link_binding(binding)
+    _note_torch()
     return LIB
 
 

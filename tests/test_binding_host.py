@@ -35,3 +35,24 @@ def test_other_calls_do_without_the_binding():
     lbuild.build()
     r = subprocess.run([sys.executable, "-c", WITHOUT], cwd=ROOT, capture_output=True, text=True)
     assert r.returncode == 0 and r.stdout.strip() == "ok", r.stderr[-800:]
+
+
+def test_the_binding_is_rebuilt_for_another_torch(monkeypatch):
+    """It links torch's internals: an unchanged source is not enough to keep it."""
+    lbuild.build()
+    done = []
+    monkeypatch.setattr(lbuild, "_compile", lambda src, verbose: pytest.fail("a CUDA source is compiled again"))
+    monkeypatch.setattr(lbuild, "_compile_binding", lambda: done.append("compile") or "binding.o")
+    monkeypatch.setattr(lbuild, "_link_binding", lambda obj: done.append("link"))
+    lbuild.build()
+    assert not done
+    real = lbuild._torch_version
+    monkeypatch.setattr(lbuild, "_torch_version", lambda: "another torch\n")
+    written = []
+    monkeypatch.setattr(lbuild, "_note_torch", lambda: written.append(1))
+    lbuild.build()
+    assert done == ["compile", "link"] and written
+    monkeypatch.setattr(lbuild, "_torch_version", real)
+    done.clear()
+    lbuild.build()
+    assert not done
