@@ -14,6 +14,7 @@
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Dtype.h>
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <string>
@@ -156,7 +157,7 @@ PyObject *object(PyObject *given, const at::Tensor &made) {
     return THPVariable_Wrap(made);
 }
 
-// Runs a call: nargs is checked, refusals become LSAError, C++ exceptions RuntimeError.
+// Runs a call: nargs is checked, refusals become LSAError, C++ exceptions what torch makes of them.
 template <class F>
 PyObject *guarded(const char *name, Py_ssize_t nargs, Py_ssize_t want, F f) {
     try {
@@ -167,10 +168,8 @@ PyObject *guarded(const char *name, Py_ssize_t nargs, Py_ssize_t want, F f) {
             PyErr_SetObject(g_error, e);
             Py_DECREF(e);
         }
-    } catch (const c10::Error &e) {      // an allocation that failed: torch's own type where it has one
-        PyErr_SetString(dynamic_cast<const c10::OutOfMemoryError *>(&e) ? PyExc_MemoryError : PyExc_RuntimeError, e.what_without_backtrace());
-    } catch (const std::exception &e) {
-        if (!PyErr_Occurred()) PyErr_SetString(PyExc_RuntimeError, e.what());
+    } catch (const std::exception &) {      // torch's own types: torch.OutOfMemoryError for an allocation that failed
+        if (!PyErr_Occurred()) torch::translate_exception_to_python(std::current_exception());
     }
     return nullptr;
 }
