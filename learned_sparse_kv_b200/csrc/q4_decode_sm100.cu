@@ -168,7 +168,7 @@ __device__ __forceinline__ int row_position(const Units &un, const DecodeParams 
     if (u >= un.total) return ABSENT;
     if (u < un.t_topk) {
         const int r = u * LSA_CHUNK + i;
-        return r < un.tk ? __ldg(p.topk_idx + (size_t)b * p.k + r) : ABSENT;
+        return r < un.tk ? max(__ldg(p.topk_idx + (size_t)b * p.k + r), -1) : ABSENT;     // -1: any negative index
     }
     return un.in_window(u, i) ? (un.first_chunk + (u - un.t_topk)) * LSA_CHUNK + i : ABSENT;
 }

@@ -5,7 +5,7 @@ import pytest
 import torch
 
 from tests import q4_reference as R
-from tests.test_gpu_q4 import _case, _run, status
+from tests.test_gpu_q4 import _case, _check, _run, status
 
 pytestmark = pytest.mark.gpu
 CH = 64
@@ -127,3 +127,15 @@ def test_a_launch_longer_than_any_wait(L):
     assert torch.equal(out[1:], out[1:2].expand(B - 1, -1, -1))
     assert float((lse[0] - lse[1] - 21 * np.log(2)).abs().max()) <= 2.0 ** -4
     assert bool(torch.isfinite(out[0]).all())
+
+
+@pytest.mark.parametrize("Hq,heads,dqk,dv,latent", SHAPES)
+def test_every_negative_index_is_flagged(L, Hq, heads, dqk, dv, latent):
+    """The smallest 32-bit integer among the top-k indices is skipped and flagged like any other negative one."""
+    c = _case(29, 2, Hq, heads, dqk, dv, latent, 70, [128, 100], [300, 65])
+    for bad in (-1, -2 ** 31):
+        c["topk"][1, 3] = bad
+        st = status()
+        out, lse = _run(L, c, st=st)
+        assert st.item() == L.DEV_INDEX, bad
+        _check(c, out, lse)
