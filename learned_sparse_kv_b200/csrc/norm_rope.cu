@@ -301,6 +301,11 @@ extern "C" int lsa_qk_norm_rope(int dtype, int64_t T, int head_dim, const void *
     auto natural = [&](const void *ptr) { return reinterpret_cast<uintptr_t>(ptr) % size == 0; };
     LSA_REQUIRE(natural(q) && natural(k) && natural(q_out) && natural(k_out) && natural(q_weight) && natural(k_weight),
                 LSA_ERR_INVALID_ARG, "lsa_qk_norm_rope: a pointer is not aligned to its element type");
+    // rows nearer to each other than their length overlap, as the rows of an expanded tensor do
+    auto apart = [&](int64_t stride, int64_t n) { return n <= 1 || stride >= head_dim || stride <= -head_dim; };
+    LSA_REQUIRE((Hq == 0 || (apart(q_out_token_stride, T) && apart(q_out_head_stride, Hq))) &&
+                    (Hk == 0 || (apart(k_out_token_stride, T) && apart(k_out_head_stride, Hk))),
+                LSA_ERR_INVALID_ARG, "lsa_qk_norm_rope: output rows overlap");
     if (T == 0) return LSA_OK;
     rope::Params p = {};
     p.q = {q, q_out, q_weight, q_token_stride, q_head_stride, q_out_token_stride, q_out_head_stride, Hq, q_norm_width, q_norm_width ? 1.f / q_norm_width : 0.f};
