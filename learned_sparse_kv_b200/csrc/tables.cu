@@ -31,10 +31,11 @@ struct Params {
     int64_t *slot_map;
     int32_t *position, *offset, *n_free;
     int32_t *status;
-    uint32_t *used;        // [ceil(n_slots / 32)]
+    uint32_t *used;        // [words()]
     int32_t *chunk_base;   // [B + 1]: new chunks before request b
     int32_t *free_list;    // [min(n_slots, B * stride)]
     int B, stride, n_slots, max_new;
+    __host__ __device__ int words() const { return (int)(((int64_t)n_slots + 31) / 32); }     // of the bitmap
 };
 
 // Lengths of request b, cut to the table: chunks to keep, chunks in all, cached and new tokens.
@@ -95,7 +96,7 @@ __global__ void __launch_bounds__(SCAN) scan_kernel(const Params p) {
         if (tokens > p.max_new) flag(p.status, LSA_DEV_CAPACITY);
     }
     int free_ = 0;
-    const int words = (p.n_slots + 31) / 32;
+    const int words = p.words();
     for (int w0 = 0; w0 < words; w0 += SCAN) {
         const int w = w0 + t;
         uint32_t bits = 0;
@@ -184,7 +185,7 @@ __global__ void __launch_bounds__(CL_THREADS, 1) cluster_kernel(const Params p) 
     const int rank = (int)cta_of_cluster(), gt = rank * CL_THREADS + t;
     constexpr int ALL = CL * CL_THREADS, WARPS = ALL / 32;
     const int gw = warp * CL + rank;      // neighbouring turns go to different CTAs
-    const int words = (p.n_slots + 31) / 32;
+    const int words = p.words();
     for (int w = gt; w < words; w += ALL) p.used[w] = 0u;
     // every CTA scans the requests for itself
     int chunks = 0;
@@ -347,7 +348,7 @@ static int launch_cluster(const Params &p, cudaStream_t stream) {
 }
 
 static size_t carve(Carver &c, Params &p) {
-    p.used = c.take<uint32_t>((p.n_slots + 31) / 32);
+    p.used = c.take<uint32_t>(p.words());
     p.chunk_base = c.take<int32_t>(p.B + 2);
     p.free_list = c.take<int32_t>(lsa_min64(p.n_slots, (int64_t)p.B * p.stride));
     return align_up(c.used, 256);
@@ -394,7 +395,7 @@ extern "C" int lsa_build_tables(const int32_t *table, int table_stride, const in
     if (B <= tables::CL_REQUESTS && (int64_t)B * table_stride <= tables::CL_ENTRIES) {
         return tables::launch_cluster(p, stream);
     }
-    LSA_CUDA(cudaMemsetAsync(p.used, 0, (size_t)(p.n_slots + 31) / 32 * 4, stream));
+    LSA_CUDA(cudaMemsetAsync(p.used, 0, (size_t)p.words() * 4, stream));
     const dim3 grid((table_stride + 255) / 256, B);
     tables::mark_kernel<<<grid, 256, 0, stream>>>(p);
     tables::scan_kernel<<<1, tables::SCAN, 0, stream>>>(p);

@@ -2,6 +2,7 @@
 import pytest
 
 from learned_sparse_kv_b200 import build as lbuild
+from learned_sparse_kv_b200 import lsa
 from tests.test_operators_host import P, refused, rope
 
 
@@ -21,3 +22,10 @@ def test_norm_rope_refuses_output_rows_that_overlap(kw):
 def test_norm_rope_strides_of_single_rows_do_not_matter():
     refused(rope(T=1, qots=0, qohs=0, eps=-1.0), 1, "eps")
     assert rope(T=0, qots=0) == 0
+
+
+def test_tables_take_every_slot_count():
+    """The bitmap's size at the largest pool, where 32-bit arithmetic would wrap."""
+    for n in (2 ** 31 - 32, 2 ** 31 - 31, 2 ** 31 - 1):
+        need = lsa.build_tables_workspace_size(4, 16, n)
+        assert 2 ** 28 <= need + 4 and need < 2 ** 28 + 4096, (n, need)
