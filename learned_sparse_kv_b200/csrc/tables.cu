@@ -292,7 +292,7 @@ __global__ void __launch_bounds__(CL_THREADS, 1) cluster_kernel(const Params p) 
         }
         before += tot;
     }
-    for (int r = n_free + gt; r < chunks; r += ALL) give(r, -1);
+    for (int64_t r = (int64_t)n_free + gt; r < chunks; r += ALL) give((int)r, -1);      // past 2^31 at the largest pools
     if (gt == 0) {
         p.n_free[0] = max(n_free - chunks, 0);
         if (n_free < chunks || tokens > p.max_new) flag(p.status, LSA_DEV_CAPACITY);
