@@ -26,7 +26,8 @@
  *     dev_status is not NULL; the affected output is truncated or the bad row
  *     is skipped.  No call traps or aborts.
  *   - Scratch memory is passed in as (ws, ws_bytes); lsa_*_workspace_size()
- *     report the size.  Workspace contents need no initialisation.
+ *     report the size.  Workspace contents need no initialisation; ws is
+ *     16-byte aligned.
  *   - Every entry point that enqueues work opens an NVTX range named after
  *     itself for the duration of the call (host side; free without a tool).
  *   - Chunk pools: token position p of sequence b lives in row p % 64 of pool
@@ -57,7 +58,7 @@ enum {
     LSA_ERR_CAPACITY = 4,       /* an output array is too small for the request */
     LSA_ERR_TIMEOUT = 5,
     LSA_ERR_TABLE = 6,          /* a host-side chunk table entry is invalid */
-    LSA_ERR_WORKSPACE = 7       /* ws_bytes smaller than the workspace query */
+    LSA_ERR_WORKSPACE = 7       /* ws_bytes smaller than the workspace query, or ws not aligned */
 };
 
 /* bits OR-ed into *dev_status by kernels */

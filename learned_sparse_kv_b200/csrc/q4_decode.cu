@@ -774,6 +774,7 @@ extern "C" int lsa_sparse_decode_q4(int q_dtype, const void *q, const uint8_t *k
     const size_t need = q4::carve(c, p, B, dv, latent);
     LSA_REQUIRE(ws && ws_bytes >= need, LSA_ERR_WORKSPACE, "lsa_sparse_decode_q4: workspace of %zu bytes, %zu needed",
                 ws_bytes, need);
+    LSA_REQUIRE(al(ws), LSA_ERR_WORKSPACE, "lsa_sparse_decode_q4: workspace not 16-byte aligned");
     p.q = q; p.k_pool = k_pool; p.v_pool = v_pool; p.table = chunk_table; p.topk_idx = topk_idx;
     p.topk_count = topk_count; p.window_start = window_start; p.window_len = window_len; p.status = dev_status;
     p.n_slots = n_slots; p.table_stride = table_stride; p.k = k;

@@ -386,6 +386,7 @@ extern "C" int lsa_build_tables(const int32_t *table, int table_stride, const in
     const size_t need = lsa_build_tables_workspace_size(B, table_stride, n_slots);
     LSA_REQUIRE(ws && ws_bytes >= need, LSA_ERR_WORKSPACE, "lsa_build_tables: workspace of %zu bytes, %zu needed",
                 ws_bytes, need);
+    LSA_REQUIRE((reinterpret_cast<uintptr_t>(ws) & 15) == 0, LSA_ERR_WORKSPACE, "lsa_build_tables: workspace not 16-byte aligned");
     tables::Params p = {};
     p.table = table; p.cached = cached_len; p.fresh = new_len; p.next = table_next; p.slot_map = slot_map;
     p.position = position; p.offset = new_offset; p.n_free = n_free; p.status = dev_status;

@@ -3,7 +3,7 @@ import pytest
 
 from learned_sparse_kv_b200 import build as lbuild
 from learned_sparse_kv_b200 import lsa
-from tests.test_operators_host import P, refused, rope
+from tests.test_operators_host import P, decode, refused, rope, tables
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -29,3 +29,10 @@ def test_tables_take_every_slot_count():
     for n in (2 ** 31 - 32, 2 ** 31 - 31, 2 ** 31 - 1):
         need = lsa.build_tables_workspace_size(4, 16, n)
         assert 2 ** 28 <= need + 4 and need < 2 ** 28 + 4096, (n, need)
+
+
+def test_workspaces_at_any_other_address_are_refused():
+    """Partials and maps are read and written as vectors: a slice of a larger buffer may begin anywhere."""
+    for off in (1, 4, 8):
+        refused(decode(ws=P + off), 7, "aligned")
+        refused(tables(ws=P + off), 7, "aligned")
