@@ -168,7 +168,7 @@ __device__ __forceinline__ int row_position(const Units &un, const DecodeParams 
     if (u >= un.total) return ABSENT;
     if (u < un.t_topk) {
         const int r = u * LSA_CHUNK + i;
-        return r < un.tk ? max(__ldg(p.topk_idx + (size_t)b * p.k + r), -1) : ABSENT;     // -1: any negative index
+        return r < un.tk ? __ldg(p.topk_idx + (size_t)b * p.k + r) : ABSENT;
     }
     return un.in_window(u, i) ? (un.first_chunk + (u - un.t_topk)) * LSA_CHUNK + i : ABSENT;
 }
@@ -176,10 +176,12 @@ __device__ __forceinline__ int row_position(const Units &un, const DecodeParams 
 __device__ __forceinline__ int row_slot(const DecodeParams &p, int b, int pos) {
     return pos >= 0 && pos / LSA_CHUNK < p.table_stride ? __ldg(p.table + (size_t)b * p.table_stride + pos / LSA_CHUNK) : -1;
 }
-// Pool row from both, -1 if the row takes no part (flagged unless it is past the set).
-__device__ __forceinline__ int64_t pool_row(const DecodeParams &p, int pos, int slot) {
+// Pool row from both, -1 if the row takes no part (flagged unless it is past the set, which is asked of the set
+// itself: ABSENT can be an index, too).
+__device__ __forceinline__ int64_t pool_row(const Units &un, const DecodeParams &p, int pos, int slot, int u, int i) {
     if (slot >= 0 && slot < p.n_slots) return (int64_t)slot * LSA_CHUNK + (pos & (LSA_CHUNK - 1));
-    if (pos != ABSENT) flag(p.status, pos < 0 ? LSA_DEV_INDEX : LSA_DEV_TABLE);
+    if (u < un.total && (u < un.t_topk ? u * LSA_CHUNK + i < un.tk : un.in_window(u, i)))
+        flag(p.status, pos < 0 ? LSA_DEV_INDEX : LSA_DEV_TABLE);
     return -1;
 }
 
@@ -242,9 +244,11 @@ __global__ void __launch_bounds__(THREADS, 1) q4_mla_kernel(const DecodeParams p
     const bool kwarp = warp >= 8 && warp < 16, vwarp = warp >= 16;
     const int w = warp & 7, quarter = lane & 3;
     const int unit_in_tile = kwarp ? (int)rank : w >> 2, first_row = kwarp ? 8 * w : 16 * (w & 3);   // in that unit
+    const int my_row = first_row + (lane & (kwarp ? 7 : 15));
     auto position = [&](int u) -> int {
-        return u < n_tiles ? row_position(un, p, b, 2 * tile_of(u) + unit_in_tile, first_row + (lane & (kwarp ? 7 : 15))) : ABSENT;
+        return u < n_tiles ? row_position(un, p, b, 2 * tile_of(u) + unit_in_tile, my_row) : ABSENT;
     };
+    auto pool_row_of = [&](int u, int pos, int slot) { return pool_row(un, p, pos, slot, 2 * tile_of(u) + unit_in_tile, my_row); };
     uint4 c[4];          // K: the four blocks of 128 columns; V: block i >> 1, row pass i & 1
     uint2 c_last;        // K: columns 512..575
     uint32_t sc[5];
@@ -282,7 +286,7 @@ __global__ void __launch_bounds__(THREADS, 1) q4_mla_kernel(const DecodeParams p
         pos2 = position(2);
         const int slot0 = row_slot(p, b, pos0);
         slot1 = row_slot(p, b, pos1);
-        row0 = pool_row(p, pos0, slot0);
+        row0 = pool_row_of(0, pos0, slot0);
         load(row0);
     }
     if (n_tiles > 0) {
@@ -426,7 +430,7 @@ __global__ void __launch_bounds__(THREADS, 1) q4_mla_kernel(const DecodeParams p
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive_cluster(full);
-            load(pool_row(p, pos1, slot1));
+            load(pool_row_of(u + 1, pos1, slot1));
             slot1 = row_slot(p, b, pos2);
             pos1 = pos2;
             pos2 = position(u + 3);
@@ -440,7 +444,7 @@ __global__ void __launch_bounds__(THREADS, 1) q4_mla_kernel(const DecodeParams p
         bool ok = true;
         post_mask(0, row0);
         for (int u = 0; u < n_tiles && ok; ++u) {
-            const int64_t next = pool_row(p, pos1, slot1);
+            const int64_t next = pool_row_of(u + 1, pos1, slot1);
             if (u + 1 < n_tiles) post_mask(u + 1, next);
             if (u > 0) ok = warp_wait(sm, &sm.pv_done[w >> 2], (u - 1) & 1, p.status);
             if (!ok) break;
