@@ -139,3 +139,51 @@ def test_every_negative_index_is_flagged(L, Hq, heads, dqk, dv, latent):
         out, lse = _run(L, c, st=st)
         assert st.item() == L.DEV_INDEX, bad
         _check(c, out, lse)
+
+
+def test_latent_two_part_tails_with_cold_caches(L):
+    """fp32 results (weights in two parts): one to five tiles a split, gathered rows first or last, nothing in the caches; no
+    wait runs out and every run gives the same bits."""
+    flush = torch.empty(2 ** 26, dtype=torch.int32, device="cuda")
+    for n, (k, n_seq) in enumerate([(0, 74), (64, 74), (200, 74), (0, 37)]):
+        rng = np.random.default_rng(n)
+        starts = rng.integers(0, 400, n_seq) * (k > 0)
+        lengths = rng.integers(0, 640, n_seq)
+        c = _case(50 + n, n_seq, 128 if n % 2 else 64, 1, 576, 512, True, k, starts, lengths)
+        st, first = status(), None
+        for _ in range(4):
+            flush.zero_()
+            out, lse = _run(L, c, torch.float32, st=st)
+            first = first or (out, lse)
+            assert torch.equal(out, first[0]) and torch.equal(lse, first[1])
+        assert st.item() == 0
+        _check(c, *first)
+
+
+@pytest.mark.parametrize("Hq,heads,dqk,dv,latent", [(5, 1, 128, 128, False), (70, 1, 576, 512, True)])
+def test_two_parts_under_a_growing_maximum(L, Hq, heads, dqk, dv, latent):
+    """Scores that grow along the sequence: both parts of the weights follow the same reference."""
+    c = _case(13, 1, Hq, heads, dqk, dv, latent, 0, [0], [2048])
+    kp = np.zeros((len(c["kp"]), 1, CH, dqk))
+    for i, s in enumerate(c["table"][0]):
+        if s >= 0:
+            kp[s, 0] = (np.arange(CH)[:, None] + CH * i) / 2048.0 * 6.0
+    c["kp"] = R.pack(*R.quantise(kp))
+    c["q"] = torch.full_like(c["q"], 1.0)
+    for dtype in (torch.float32, torch.float16):
+        _check(c, *_run(L, c, dtype))
+
+
+def test_two_part_wait_that_runs_out(L):
+    """The failure path with fp32 results: LSA_DEV_TIMEOUT, and the next call gives the bits of the one before."""
+    c = _case(31, 2, 128, 1, 576, 512, True, 64, [640, 128], [700, 900])
+    good = _run(L, c, torch.float32)
+    st = status()
+    L.test_stall_next_wait(L.TEST_STALL_ATTENTION_Q4)
+    _run(L, c, torch.float32, st=st)
+    torch.cuda.synchronize()
+    assert st.item() & L.DEV_TIMEOUT
+    st.zero_()
+    again = _run(L, c, torch.float32, st=st)
+    assert st.item() == 0
+    assert torch.equal(again[0], good[0]) and torch.equal(again[1], good[1])
