@@ -66,8 +66,8 @@ __device__ __forceinline__ float max_nan(float a, float b) {
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
     return d;
 }
-// The 16 highest significant bits.
-__device__ __forceinline__ float cut16(float x) { return __uint_as_float(__float_as_uint(x) & ~0x7fu); }
+// The 17 highest significant bits (16 of them stored).
+__device__ __forceinline__ float cut17(float x) { return __uint_as_float(__float_as_uint(x) & ~0x7fu); }
 
 // Half a group: eight values as four code bytes and, in scale_byte, the scale of the whole group, whose other half
 // is with the neighbouring lane (lane ^ 1; both call together).
@@ -79,8 +79,9 @@ __device__ __forceinline__ float cut16(float x) { return __uint_as_float(__float
 // s g has 4): a quotient X / S 2^k that is not the halfway point T 2^m is off it by at least 2^-11 of its
 // size, because X 2^a and S T are whole numbers below 2^11 when both are scaled to the same size
 // (T <= 7 and S <= 15 for the codes, T <= 31 and S = 6 for the scale).  The product with the approximate
-// reciprocal is off by less than 2^-21; made larger by 2^-17 and cut to 16 significant bits it is the
-// halfway point again where the quotient is, and nothing else crosses one.
+// reciprocal is off by less than 2^-22; made larger by 2^-17 and cut to 17 significant bits it is the
+// halfway point again where the quotient is (a halfway point is at most 31/16 of a power of two, and 31/16 (2^-17 +
+// 2^-22) < 2^-16), and nothing else crosses one.
 template <bool EXACT>
 __device__ __forceinline__ uint32_t quantise_half(const float (&x)[8], float g, float g6, uint32_t &scale_byte) {
     float amax = 0.f;
@@ -90,7 +91,7 @@ __device__ __forceinline__ uint32_t quantise_half(const float (&x)[8], float g, 
     constexpr float UP = 1.f + 0x1p-17f;
     float t;
     if constexpr (EXACT) t = __fdiv_rn(amax, g6);
-    else t = cut16(amax * (UP * g6));           // g6: 1 / (6 g) here
+    else t = cut17(amax * (UP * g6));           // g6: 1 / (6 g) here
     uint16_t e;
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(e) : "f"(0.f), "f"(fminf(t, E4M3_MAX)));
     const float sg = __half2float(__ushort_as_half((uint16_t)e4m3x2_to_f16(e))) * g;
@@ -105,7 +106,7 @@ __device__ __forceinline__ uint32_t quantise_half(const float (&x)[8], float g, 
         asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(sg));
         r *= UP;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] = cut16(x[i] * r);
+        for (int i = 0; i < 8; ++i) y[i] = cut17(x[i] * r);
     }
     uint32_t w;
     asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"

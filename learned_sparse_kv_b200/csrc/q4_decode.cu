@@ -24,9 +24,11 @@
 // and its merge take: otherwise one CTA could be dealt all of the shortest sequences (16 sequences of 1 to
 // 16K tokens, 8 K/V heads: 41.6 us without).  A segment that lies inside one range is finished there; the at most two
 // that a CTA shares with others leave partials for a second kernel.
-// Measured on the device, both kernels: one sequence of 524,288 tokens, 32 heads over 4: 63.4 us for 302 MB, 4.8 of 6.55 TB/s
-// (conversions, mma.sync and copies share the issue slots); 16 sequences of 1 to 16K tokens, 8 K/V heads: 18.9 us
-// for 37 MB; one sequence of 8,512 rows, 16 heads on one: 12.8 us, all of it latency (lengths, positions, slots, rows,
+// Measured on the device, both kernels, bf16 and f16 results (the second with weights in two parts): one sequence of
+// 524,288 tokens, 32 heads over 4: 64.4 and 70.7 us for 302 MB, 4.7 and 4.3 of 6.55 TB/s (conversions, mma.sync and copies
+// share the issue slots); 16 sequences of 1 to 16K tokens, 8 K/V heads: 19.0 and 20.2 us for 37 MB (rows of 64: 16.1 for
+// half the bytes); 4 of 32K, 16 and 32 heads on one: 17.1 and 22.6 us, since more than 16 heads read the pool again;
+// one sequence of 8,512 rows, 16 heads on one: 12.8 us, all of it latency (lengths, positions, slots, rows,
 // the merge: loads that wait for each other).
 #include "block_scan.cuh"
 #include "nvtx_range.cuh"

@@ -14,7 +14,7 @@
 //               128r..128r+127 and 256+128r.. (64 KB)
 // N = 128 because a pair MMA costs the same 45 cycles at N = 64 and at N = 128.  With Q (72 KB) and P
 // (16 KB) that is all of shared memory, so K and V have one stage each, handed over in parts: K
-// in three groups of 192 columns, V and P unit by unit.  A part of the next tile is written
+// in groups of 256, 256 and 64 columns, V and P unit by unit.  A part of the next tile is written
 // as soon as the MMAs that read it are done, while the MMAs of the other parts run.  The
 // codes of the next tile are in registers by then, the slots of the one after are being loaded.
 // TMEM per CTA: two S buffers of 64 columns and O = 64 heads x 512 values in 256 columns.
@@ -24,11 +24,11 @@
 //   8..15  dequantise K                    16..23  dequantise V, row masks; both write O at the end
 // (Eight warps each: with four the conversion, a chain of dependent instructions, took 3000
 // cycles a tile and paced the pipeline while the issue slots were 25 % used.)
-// Measured on the device, merge included: 8 sequences of 10,048 rows, 128 heads: 37.9 us (591 TFLOP/s); 32 such
-// sequences, 64 heads: 120 us.  A tile takes 4,400 cycles for 2,640 of MMAs timed alone: operand reads (240 KB a
-// tile and CTA) and the conversion's stores (152 KB) share the shared-memory pipe, 128 bytes a cycle, and
-// while the conversion stores an MMA of Q K^T takes 72 cycles instead of 45.  So what shortens other
-// chains does not help: eight softmax warps of 32 columns a thread 41.2 us, rows looked up by one warp for
+// Measured on the device, merge included: 8 sequences of 10,048 rows, 128 heads: 38.8 us (577 TFLOP/s), with weights in
+// two parts 49.2; 32 such sequences, 64 heads: 122.5 and 168 us.  A tile takes 4,400 cycles for 2,640 of MMAs timed
+// alone: operand reads (240 KB a tile and CTA) and the conversion's stores (152 KB) share the shared-memory pipe, 128
+// bytes a cycle, which is 3,060 of them, and while the conversion stores an MMA of Q K^T takes 72 cycles instead of
+// 45.  What shortens other chains did not help: eight softmax warps of 32 columns a thread 41.2 us, rows looked up by one warp for
 // all 40.0, loads of a row by 12 neighbouring lanes 42.9.  A launch spends 9,000 cycles on its prologue
 // (lengths, positions, slots, codes: loads that wait for each other).
 // Every mbarrier wait is bounded, each by itself and never the launch as a whole: on timeout the kernel sets
@@ -681,7 +681,8 @@ __global__ void __launch_bounds__(THREADS, 1) q4_mla_kernel(const DecodeParams p
     }
 }
 
-// Splits per sequence: one CTA pair each, all co-resident; a single sequence takes half the pairs.
+// Splits per sequence: one CTA pair each, all co-resident; a single sequence takes half the pairs.  Both sides of
+// that, one sequence of 128 heads, half and all: 10K rows 23.9 and 24.6 us, 32K 34.1 and 31.0, 128K 84.9 and 56.2.
 int splits(int B, int max_units) {
     const int clusters = sm_count() / 2, tiles = (max_units + 1) / 2;
     return max(1, min(min(clusters / max(B, 1), clusters / 2), tiles));

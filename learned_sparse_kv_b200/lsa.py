@@ -518,7 +518,8 @@ def build_tables(table, cached_len, new_len, n_slots, max_new, *, table_next=Non
 
     table [B, stride] int32 (-1: none), cached_len, new_len [B] int32.  Returns (table_next [B, stride] int32,
     slot_map [max_new] int64, position [max_new] int32, new_offset [B + 1] int32, n_free [1] int32); map entries behind
-    the last new token are -1.
+    the last new token are -1.  Requests may share full chunks; a chunk that is only partly filled and shared is the
+    caller's to copy, since a new token is written into it (no status bit tells of it).
     """
     if stream is not None:
         return _on_stream(stream, _native.build_tables, table, cached_len, new_len, n_slots, max_new, table_next, slot_map,
