@@ -5,7 +5,7 @@
 // A thread owns half a group, eight values: 16 bytes of a bf16 row, 4 code bytes; the two lanes of a
 // group exchange their maxima.  A thread keeps its place in the row (side, head, columns) and walks
 // the tokens, so that no division is left in the loop.  2 + 0.5625 bytes a bf16 value would bound it by
-// memory; measured, 16,384 tokens of 8 heads of 128, K and V, written and read back: 44 to 45.6 us by box for 172 MB,
+// memory; measured, 16,384 tokens of 8 heads of 128, K and V, written and read back: 44 to 45.6 us for 172 MB,
 // 3.8 of 6.55 TB/s: the rounding takes about 9 instructions a value, and the write has 55 % of the issue slots busy.
 // 32 latent rows appended with their indexer keys: 3 us.
 #include "nvtx_range.cuh"

@@ -12,8 +12,8 @@
 // separated by cluster barriers: clear the bitmap of used slots | mark the kept ones and copy their
 // entries | count the free ones | give as many as are needed to the new chunks | write the maps.
 // Larger problems use all multiprocessors: five launches (clear, mark, scan by one CTA, tables,
-// maps).  32 requests of 16K to 512K tokens (1 MB of tables, 73K kept chunks): 14.4 to 15.2 us on the device by
-// box (five launches: 14.5), of which the marks, one atomic a chunk on a bitmap in L2, take 5; 4096 requests, 1.05M
+// maps).  32 requests of 16K to 512K tokens (1 MB of tables, 73K kept chunks): 14.4 to 15.2 us on the device
+// (five launches: 14.5), of which the marks, one atomic a chunk on a bitmap in L2, take 5; 4096 requests, 1.05M
 // kept chunks, five launches: 56 us.
 #include <limits.h>
 

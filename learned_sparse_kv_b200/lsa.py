@@ -533,9 +533,10 @@ def qk_norm_rope(q, k, position, inv_freq, *, q_weight=None, k_weight=None, q_no
     """RMS norm of q and k for each head and position rotation, in one pass.
 
     q [T, Hq, D], k [T, Hk, D] (bf16, f16 or fp32, columns contiguous; k may be None), position [T] int32 (negative:
-    padding, the output row stays as it is), inv_freq [rot_dim / 2] fp32.  The norm covers the first q_norm_width /
-    k_norm_width columns (default: the weight's length, or none without a weight); the rotation covers columns
-    [rot_offset, rot_offset + rot_dim).  Returns (q_out, k_out); outputs may be the inputs.
+    padding, the output row stays as it is, so it is uninitialised where the call allocates the output), inv_freq
+    [rot_dim / 2] fp32.  The norm covers the first q_norm_width / k_norm_width columns (default: the weight's length, or
+    none without a weight); the rotation covers columns [rot_offset, rot_offset + rot_dim).  Returns (q_out, k_out);
+    outputs may be the inputs, and their rows must not overlap.
     """
     if stream is not None:
         return _on_stream(stream, _native.qk_norm_rope, q, k, position, inv_freq, q_weight, k_weight, q_norm_width,

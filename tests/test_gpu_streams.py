@@ -92,3 +92,25 @@ def test_outputs_dropped_while_the_callers_stream_reads_them(L, name):
     for a, b in zip(copies, ref):
         assert torch.equal(a, b)
     del junk
+
+
+@pytest.mark.parametrize("name", NAMES)
+def test_calls_on_a_side_stream_captured(L, name):
+    """A capture that forks to a side stream and joins it again: replays give the eager call's bits."""
+    call, _ = _calls(L)[name]
+    ref = call()
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        main = torch.cuda.current_stream()
+        side.wait_stream(main)
+        out = call(stream=side)
+        main.wait_stream(side)
+    for t in out:
+        t.zero_()
+    for _ in range(3):
+        g.replay()
+    torch.cuda.synchronize()
+    for a, b in zip(out, ref):
+        assert torch.equal(a, b)
