@@ -480,7 +480,7 @@ size_t lsa_build_tables_workspace_size(int B, int table_stride, int64_t n_slots)
  * Angles are reduced in 64 bits, everything else is fp32, rounded once to the rows' type.
  * Rows whose position is negative are padding: nothing of them is read into a result and their
  * output rows stay as they are.  q_out may be q and k_out may be k; outputs must not overlap inputs
- * in any other way.
+ * in any other way, nor their rows one another (strides below head_dim are refused).
  *   q, k, q_out, k_out: strides in elements for tokens and heads, columns contiguous; Hq or Hk may be 0
  *   weights [norm_width] of the rows' type; position [T] int32, inv_freq [rot_dim / 2] fp32 (device)
  * Supported: bf16, f16, fp32; even head_dim up to 1024; even rot_offset and rot_dim; up to 1024 heads.
